@@ -306,6 +306,96 @@ MOE_EXPORT moe_status_t moe_gather_rows(const void* src, int64_t src_rows, const
                                         int64_t row_bytes, void* dst, void* workspace, size_t ws_bytes,
                                         moe_stream_t stream);
 
+/* ---- Routing and combine of any E and k -------------------------------------
+ * The sublayer above fixes E = 8, k = 2 and the softmax router. The calls below
+ * route and combine for other routers, and give the router's gradient for
+ * training. They follow the file header's rules
+ * (dense, row-major, 16-byte aligned device arrays; checks on the host; no
+ * synchronisation; nothing kept between calls); calls that may overlap on the
+ * GPU need distinct workspaces and outputs. */
+
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0, /* s = softmax(logits) over the E experts */
+  MOE_SCORE_SIGMOID = 1  /* s = 1 / (1 + exp(-logit)) per expert   */
+} moe_score_t;
+
+typedef enum {
+  MOE_GROUP_MAX = 0,      /* a group's value: its largest rank value                  */
+  MOE_GROUP_TOP2_SUM = 1  /* the sum of its two largest score + bias (of the one it has) */
+} moe_group_rule_t;
+
+/* Routing of T tokens from their router logits. Per token:
+ *   a logit that is -inf or NaN masks its expert (score 0, never chosen); +inf
+ *   counts as the largest fp32; s = the scores of the rest (moe_score_t);
+ *   rank value c = s + bias, or the logit itself without a bias (same order);
+ *   with n_groups > 1 the E experts form n_groups runs of E / n_groups, and only
+ *   the topk_groups groups of the largest value stay (ties: the lower group);
+ *   idx = the k largest c in descending order, ties to the lower expert;
+ *   weights = scale * s[idx], divided by their sum if renormalize == 1.
+ * The bias steers the choice only. The choice is that of the values in 64 bits:
+ * where 32 bits cannot decide, the kernel decides in 64. A token with fewer than
+ * k experts to choose from gets idx -1 and weight 0 in the slots left over.
+ * Limits: 1 <= E <= 1024, 1 <= k <= min(E, 32), 1 <= topk_groups <= n_groups <= 32,
+ * E % n_groups == 0, 0 <= T <= 2^24, scale finite. */
+typedef struct {
+  const void* logits;        /* [T, E] MOE_F32 or MOE_BF16                               */
+  const float* bias;         /* [E] fp32 or NULL; an expert with a NaN bias is masked     */
+  const int32_t* n_tokens;   /* one int32 on the device, or NULL for T: rows from it on are
+                                padding (idx -1, weights and scores 0, not dispatched)    */
+  int64_t T;
+  int32_t E, k;
+  moe_dtype_t dtype;         /* of the logits                                             */
+  moe_score_t score;
+  int32_t n_groups, topk_groups; /* 1, 1: no groups                                       */
+  moe_group_rule_t group_rule;
+  int32_t renormalize;       /* 0 or 1                                                    */
+  float scale;
+} moe_topk_args_t;
+
+/* Outputs. The dispatch arrays (counts .. gate_perm) are all given or all NULL;
+ * permuted order = chosen slots sorted by (expert, token), as moe_routed_t's. */
+typedef struct {
+  int32_t* idx;        /* [T, k] chosen experts, -1 = none                              */
+  float* weights;      /* [T, k]                                                         */
+  float* scores;       /* [T, E] scores of every expert, or NULL                         */
+  int32_t* counts;     /* [E]    slots per expert                                        */
+  int32_t* offsets;    /* [E+1]  exclusive prefix of counts                              */
+  int32_t* perm_token; /* [T*k]  token of each permuted row, -1 behind the last one       */
+  int32_t* perm_slot;  /* [T*k]  its slot, -1 behind the last one                         */
+  int32_t* slot_pos;   /* [T, k] permuted row of each slot, -1 = none                    */
+  float* gate_perm;    /* [T*k]  weight of each permuted row, 0 behind the last one       */
+} moe_topk_routed_t;
+
+/* Workspace bytes of moe_topk_route: 0 when none is needed (no dispatch arrays
+ * asked for, or a batch of one block) and on bad sizes. */
+MOE_EXPORT size_t moe_topk_workspace_size(int64_t T, int32_t E, int32_t k);
+
+/* See moe_topk_args_t. `workspace` may be NULL when the size above is 0. */
+MOE_EXPORT moe_status_t moe_topk_route(const moe_topk_args_t* args, const moe_topk_routed_t* routed,
+                                       void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/* Gradient of moe_topk_route's weights, and optionally of its scores, with
+ * respect to the logits, for the choice `idx` it made (the choice itself has no
+ * gradient; the bias takes none). args as given to moe_topk_route; bias and the
+ * group fields are not looked at. Entries of idx outside [0, E) contribute nothing;
+ * masked logits and padded rows get 0. Sums in fp32, fixed order, no atomics. */
+MOE_EXPORT moe_status_t moe_topk_route_backward(const moe_topk_args_t* args,
+                                                const int32_t* idx,          /* [T, k]               */
+                                                const float* grad_weights,   /* [T, k]               */
+                                                const float* grad_scores,    /* [T, E] or NULL       */
+                                                void* grad_logits,           /* [T, E], logits' type */
+                                                moe_stream_t stream);
+
+/* out[t] = residual[t] + sum over the k slots of weights[t, s] * y[slot_pos[t, s]],
+ * summed in fp32 in slot order and rounded once. y [R, d] and out [T, d] are MOE_F32
+ * or MOE_BF16 (residual has out's type); weights [T, k] fp32 or NULL for 1; a slot_pos
+ * outside [0, R) adds nothing. Limits: 0 <= T <= 2^24, 1 <= k <= 32, d a multiple of 8,
+ * 0 <= R <= 2^29. Generalises moe_combine (k = 2, fp32 rows). */
+MOE_EXPORT moe_status_t moe_combine_topk(const void* y, moe_dtype_t y_dtype, int64_t R, const int32_t* slot_pos,
+                                         const float* weights, int64_t T, int32_t k, int64_t d,
+                                         const void* residual, void* out, moe_dtype_t out_dtype,
+                                         moe_stream_t stream);
+
 /* Passage: as moe_forward; the options follow Grok-1 book ch. 10, section
  * 10.3.1 (Mixtral renormalisation, sandwich post-norm) and section 10.4 (SiLU).
  * Forward pass on a caller-provided device workspace of ws_bytes bytes

@@ -23,6 +23,8 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_MISALIGNED = 0, 1, 2, 
 MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE_CHECK = 4, 5, 6
 MOE_F32, MOE_BF16, MOE_BF16_INT8W = 0, 1, 2
 MOE_ACT_GELU_TANH, MOE_ACT_GELU_ERF, MOE_ACT_SILU = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2_SUM = 0, 1
 MOE_PATH_AUTO, MOE_PATH_TOKEN_TILE, MOE_PATH_WEIGHT_STREAM, MOE_PATH_TOKEN_TILE_SINGLE = 0, 1, 2, 3
 
 # Every function include/moe.h exports, with (restype, argtypes).
@@ -64,6 +66,18 @@ class MoeExpertRows(ctypes.Structure):
                 ("R", c_int64), ("d", c_int64), ("f", c_int64), ("n_experts", c_int32), ("dtype", c_int)]
 
 
+class MoeTopkArgs(ctypes.Structure):
+    _fields_ = [("logits", c_void_p), ("bias", c_void_p), ("n_tokens", c_void_p), ("T", c_int64), ("E", c_int32),
+                ("k", c_int32), ("dtype", c_int), ("score", c_int), ("n_groups", c_int32), ("topk_groups", c_int32),
+                ("group_rule", c_int), ("renormalize", c_int32), ("scale", c_float)]
+
+
+class MoeTopkRouted(ctypes.Structure):
+    _fields_ = [("idx", c_void_p), ("weights", c_void_p), ("scores", c_void_p), ("counts", c_void_p),
+                ("offsets", c_void_p), ("perm_token", c_void_p), ("perm_slot", c_void_p), ("slot_pos", c_void_p),
+                ("gate_perm", c_void_p)]
+
+
 EXPORTS.update({
     "moe_forward": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, POINTER(MoeScales), c_void_p,
                             c_int64, c_int64, c_int64, c_int32, c_int32, c_int, c_void_p]),
@@ -86,6 +100,11 @@ EXPORTS.update({
                             c_void_p, c_size_t, c_void_p]),
     "moe_gather_rows": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_size_t,
                                 c_void_p]),
+    "moe_topk_workspace_size": (c_size_t, [c_int64, c_int32, c_int32]),
+    "moe_topk_route": (c_int, [POINTER(MoeTopkArgs), POINTER(MoeTopkRouted), c_void_p, c_size_t, c_void_p]),
+    "moe_topk_route_backward": (c_int, [POINTER(MoeTopkArgs), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_combine_topk": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_void_p, c_int64, c_int32, c_int64, c_void_p,
+                                 c_void_p, c_int, c_void_p]),
 })
 
 _LIB = None

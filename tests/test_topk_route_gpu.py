@@ -1,0 +1,376 @@
+"""moe_topk_route, its backward pass and moe_combine_topk on the GPU against 64-bit
+references: choices and dispatch exactly, numbers to bounds counted in fp32
+roundings (u = 2^-24) of the formula, plus the rounding of the output's type."""
+
+import numpy as np
+import pytest
+import torch
+
+import _routed_reference as ref
+import mixture_experts_ffn_14_b200 as moe
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+SCORE = {"softmax": moe.MOE_SCORE_SOFTMAX, "sigmoid": moe.MOE_SCORE_SIGMOID}
+RULE = {"max": moe.MOE_GROUP_MAX, "top2": moe.MOE_GROUP_TOP2_SUM}
+INTS = ("idx", "counts", "offsets", "perm_token", "perm_slot", "slot_pos")
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def logits_of(T, E, dtype, seed, masked=0.0, std=1.5):
+    g = gen(seed)
+    l = torch.randn((T, E), generator=g, device=DEV) * std
+    if masked:
+        l[torch.rand((T, E), generator=g, device=DEV) < masked] = -float("inf")
+        l[torch.rand(T, generator=g, device=DEV) < 0.1] = -float("inf")     # rows with nothing left
+        l[torch.rand((T, E), generator=g, device=DEV) < 0.05] = float("nan")
+    return l.to(dtype)
+
+
+def spread(l, idx):
+    """Largest difference of a row's chosen logits, capped where exp underflows."""
+    has = (idx >= 0) & (idx < l.shape[1])
+    a = np.take_along_axis(l, np.where(has, idx, 0), 1)
+    hi = np.where(has & np.isfinite(a), a, -np.inf).max(1)
+    lo = np.where(has & np.isfinite(a), a, np.inf).min(1)
+    with np.errstate(invalid="ignore"):
+        d = np.where(np.isfinite(hi) & np.isfinite(lo), hi - lo, 0)
+    return np.minimum(d, 110)[:, None]
+
+
+def weight_bound(l, r, kind, renorm):
+    """Relative error of a weight, in u. Sigmoid: expf 2, sum 1, quotient 1, scale 1.
+    Softmax: expf 2, its argument's rounding, 37 for the sum of 1024 terms, quotient 1,
+    scale 1. Renormalised: both of the above on the k shares instead, whose sum has 5
+    levels, numerator and denominator alike."""
+    if renorm:
+        return (20 + 2 * spread(l, r["idx"])) * U
+    if kind == "sigmoid":
+        return np.full((l.shape[0], 1), 8 * U)
+    top = np.where(np.isfinite(l), l, -np.inf).max(1, keepdims=True)
+    low = np.where(np.isfinite(l), l, np.inf).min(1, keepdims=True)
+    with np.errstate(invalid="ignore"):
+        return (50 + np.nan_to_num(np.minimum(np.abs(top - low), 110))) * U
+
+
+def run_and_check(logits, k, kind, bias=None, groups=1, keep=1, rule="max", renorm=False, scale=1.0, n=None,
+                  want_scores=False, n_tokens=None, **kw):
+    got = moe.moe_topk_route(logits, k, score=SCORE[kind], bias=bias, n_groups=groups, topk_groups=keep,
+                             group_rule=RULE[rule], renormalize=renorm, scale=scale, want_scores=want_scores,
+                             n_tokens=n_tokens, **kw)
+    torch.cuda.synchronize()
+    check(got, logits, k, kind, bias, groups, keep, rule, renorm, scale, n)
+    return got
+
+
+def check(got, logits, k, kind, bias=None, groups=1, keep=1, rule="max", renorm=False, scale=1.0, n=None):
+    l = logits.double().cpu().numpy()
+    r = ref.route(l, k, kind, None if bias is None else bias.double().cpu().numpy(), groups, keep, rule, renorm,
+                  scale, n)
+    for name in INTS:
+        if name in got:
+            a = got[name].cpu().numpy()
+            assert (a == r[name]).all(), (name, np.argwhere(a != r[name])[:5])
+    bound = weight_bound(l, r, kind, renorm)
+    w = got["weights"].double().cpu().numpy()
+    assert (np.abs(w - r["weights"]) <= bound * np.abs(r["weights"]) + 1e-37).all()
+    if "gate_perm" in got:
+        assert torch.equal(got["gate_perm"].cpu(), torch.from_numpy(ref.dispatch(r["idx"], w, l.shape[1])["gate_perm"]).float())
+    if "scores" in got:
+        s = got["scores"].double().cpu().numpy()
+        assert (np.abs(s - r["scores"]) <= weight_bound(l, r, kind, False) * r["scores"] + 1e-37).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k", [
+    (1, 1, 1), (1, 8, 2), (31, 2, 2), (32, 8, 1), (33, 33, 5), (64, 60, 6), (65, 64, 8), (100, 96, 4), (257, 160, 6),
+    (40, 256, 8), (70, 500, 9), (35, 512, 10), (50, 1000, 32), (33, 1024, 32), (2100, 16, 2)])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_sizes(T, E, k, kind, dtype):
+    l = logits_of(T, E, dtype, 1000 + T + E)
+    bias = torch.randn(E, generator=gen(E), device=DEV) * 0.1
+    run_and_check(l, k, kind, want_scores=True)
+    run_and_check(l, k, kind, bias=bias, renorm=True, scale=2.5)
+
+
+@pytest.mark.parametrize("E,groups,keep", [(8, 2, 1), (8, 8, 3), (64, 4, 2), (60, 4, 2), (96, 3, 2), (160, 8, 3),
+                                           (256, 8, 4), (256, 32, 5), (512, 16, 16), (1000, 10, 4), (1024, 2, 1)])
+@pytest.mark.parametrize("rule", ["max", "top2"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_groups(E, groups, keep, rule, with_bias, kind):
+    k = min(8, max(1, E // groups * keep - 1))
+    bias = torch.randn(E, generator=gen(E), device=DEV) * 0.1 if with_bias else None
+    l = logits_of(70, E, torch.bfloat16, E + groups, masked=0.2)
+    run_and_check(l, k, kind, bias=bias, groups=groups, keep=keep, rule=rule, renorm=True)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,k", [(8, 3), (96, 16), (256, 8)])
+def test_route_masked_rows_and_odd_values(kind, renorm, E, k):
+    l = logits_of(90, E, torch.float32, E + k, masked=0.5)
+    l[5] = torch.finfo(torch.float32).min          # the type's lowest value everywhere
+    l[6] = float("inf")                            # all the largest
+    l[7, :] = -float("inf")
+    l[7, E // 2] = 1.0                             # one expert left
+    l[8] = 0.0
+    l[9, ::2] = -0.0                               # equal values of either sign of zero
+    l[9, 1::2] = 0.0
+    l[10] = -200.0                                 # scores below the fp32 range
+    l[11] = 200.0
+    l[12] = torch.arange(E, device=DEV) * -30.0
+    for bias in (None, torch.zeros(E, device=DEV), torch.randn(E, generator=gen(3), device=DEV)):
+        run_and_check(l, k, kind, bias=bias, renorm=renorm, want_scores=True)
+    bias = torch.randn(E, generator=gen(4), device=DEV)
+    bias[0], bias[1], bias[2] = float("nan"), -float("inf"), float("inf")
+    run_and_check(l, k, kind, bias=bias, renorm=renorm)
+    if E % 8 == 0:
+        run_and_check(l, k, kind, bias=bias, renorm=renorm, groups=8, keep=3, rule="max")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_ties_and_near_ties_go_by_64_bits(kind, dtype):
+    # Few distinct logits: ties everywhere, decided by the lower expert.
+    E, k = 128, 8
+    l = torch.randint(-2, 3, (100, E), generator=gen(8), device=DEV).to(dtype)
+    run_and_check(l, k, kind)
+    run_and_check(l, k, kind, bias=torch.zeros(E, device=DEV), groups=8, keep=2, rule="top2")
+    # score + bias equal up to the rounding of the bias: fp32 cannot order them
+    row = (torch.randn(E, generator=gen(9), device=DEV)).to(dtype)
+    _, _, s = ref.scores(row.double().cpu().numpy()[None], kind)
+    bias = torch.from_numpy((1.0 - s[0]).astype(np.float32)).to(DEV)
+    l = row.repeat(40, 1)
+    run_and_check(l, k, kind, bias=bias)
+    run_and_check(l, k, kind, bias=bias, groups=16, keep=5, rule="top2")
+    run_and_check(l, k, kind, bias=bias, groups=16, keep=5, rule="max", renorm=True)
+
+
+@pytest.mark.parametrize("n", [0, 1, 37, 64, 100, 500, -3])
+@pytest.mark.parametrize("T", [20, 100])
+def test_route_padded_batch(T, n):
+    l = logits_of(T, 64, torch.bfloat16, 5)
+    l[max(0, min(n, T)):] = float("nan")           # whatever stands behind the last token
+    nt = torch.tensor([n], dtype=torch.int32, device=DEV)
+    run_and_check(l, 6, "sigmoid", renorm=True, n=n, n_tokens=nt, want_scores=True)
+
+
+def test_route_without_dispatch_and_with_given_outputs():
+    l = logits_of(200, 64, torch.float32, 6)
+    full = run_and_check(l, 4, "softmax")
+    bare = moe.moe_topk_route(l, 4, dispatch=False)
+    assert set(bare) == {"idx", "weights"}
+    assert torch.equal(bare["idx"], full["idx"]) and torch.equal(bare["weights"], full["weights"])
+    out = {n: torch.full_like(t, 77) for n, t in full.items()}
+    ws = torch.full((moe.moe_topk_workspace_size(200, 64, 4),), 255, dtype=torch.uint8, device=DEV)
+    got = moe.moe_topk_route(l, 4, out=out, workspace=ws)
+    for name in out:
+        assert got[name] is out[name] and torch.equal(got[name], full[name])
+    assert moe.moe_device_status(ws) == (0, 0)
+    with pytest.raises(ValueError):
+        moe.moe_topk_route(l, 4, out={"scores": torch.empty(200, 64, device=DEV)})
+    with pytest.raises(ValueError):
+        moe.moe_topk_route(l, 4, out={"idx": torch.empty(200, 5, dtype=torch.int32, device=DEV)})
+    with pytest.raises(ValueError):
+        moe.moe_topk_route(l.t(), 4)
+    with pytest.raises(moe.MoeError):
+        moe.moe_topk_route(l, 4, workspace=ws[:256])
+    with pytest.raises(moe.MoeError):
+        moe.moe_topk_route(l, 65)
+
+
+def test_route_empty_batch():
+    l = torch.empty((0, 16), device=DEV)
+    r = moe.moe_topk_route(l, 2)
+    assert r["counts"].tolist() == [0] * 16 and r["offsets"].tolist() == [0] * 17 and r["idx"].shape == (0, 2)
+    g = moe.moe_topk_route_backward(l, r["idx"], r["weights"])
+    assert g.shape == (0, 16)
+
+
+def test_route_matches_the_sublayers_router():
+    # The same logits give the same choice and gates as moe_route_dispatch (E = 8, k = 2).
+    from mixture_experts_ffn_14_b200 import expert_parallel as EP
+
+    T, d = 150, 256
+    x = torch.randn((T, d), generator=gen(11), device=DEV)
+    wr = torch.zeros((d, 8), device=DEV)
+    wr[torch.arange(8), torch.arange(8)] = 1.0      # logits = x[:, :8] exactly
+    comp = EP.LibraryCompute(wr, torch.empty((8, d, 64), device=DEV), None, None)
+    a = comp.route_dispatch(x)
+    b = moe.moe_topk_route(x[:, :8].contiguous(), 2)
+    for n, m in (("idx", "idx"), ("counts_dev", "counts"), ("offsets", "offsets"), ("perm_token", "perm_token"),
+                 ("perm_slot", "perm_slot"), ("slot_pos", "slot_pos")):
+        assert torch.equal(a[n], b[m]), n
+    assert (a["gates"] - b["weights"]).abs().max() <= 120 * U   # both within 60 u of the exact value <= 1
+
+
+# ------------------------------------------------------------------ backward --
+
+def grad_bound(l, idx, gw, kind, renorm, scale, gs, n):
+    """Bound of the fp32 error of each gradient: the roundings of one weight (weight_bound)
+    on every term, and of the sums over the k chosen (k) and the E scores (37)."""
+    T, E = l.shape
+    lc, masked, s = ref.scores(l, kind)
+    c = (120 + 2 * spread(l, idx) + idx.shape[1]
+         + (np.minimum(np.where(masked, 0, np.abs(lc)).max(1, keepdims=True), 110) * 2 if kind == "softmax" else 0)) * U
+    has = (idx >= 0) & (idx < E)
+    g = np.where(has, np.abs(gw), 0) * abs(scale)
+    size = np.zeros((T, E))
+    p, _ = ref.weights_of(l, idx, kind, renorm, 1.0)
+    each = p * (g + (g * p).sum(1, keepdims=True)) if renorm else g
+    with np.errstate(over="ignore"):
+        rest = 1 / (1 + np.exp(lc))
+    ds = np.zeros((T, E)) if gs is None else np.abs(gs)
+    direct = np.zeros((T, E))
+    for t in range(T):
+        for j in np.nonzero(has[t])[0]:
+            (direct if renorm else ds)[t, idx[t, j]] += each[t, j]
+    if kind == "sigmoid":
+        size = s * rest * ds + direct * rest
+    else:
+        size = s * (ds + (s * ds).sum(1, keepdims=True)) + direct
+    return c * size + 1e-36
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (33, 33, 5), (64, 60, 6), (100, 256, 8), (20, 512, 10), (17, 1000, 32)])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_backward(T, E, k, kind, renorm, dtype):
+    l = logits_of(T, E, dtype, T + E + k, masked=0.2 if E > 8 else 0.0)
+    l64 = l.double().cpu().numpy()
+    g = gen(T * 7 + E)
+    gw = torch.randn((T, k), generator=g, device=DEV)
+    for gs in (None, torch.randn((T, E), generator=g, device=DEV)):
+        n = T - T // 4
+        idx = moe.moe_topk_route(l, k, score=SCORE[kind], dispatch=False)["idx"]
+        got = moe.moe_topk_route_backward(l, idx, gw, score=SCORE[kind], renormalize=renorm, scale=1.5, grad_scores=gs,
+                                          n_tokens=torch.tensor([n], dtype=torch.int32, device=DEV))
+        a = (l64, idx.cpu().numpy(), gw.double().cpu().numpy(), kind, renorm, 1.5,
+             None if gs is None else gs.double().cpu().numpy(), n)
+        want = ref.route_backward(*a)
+        lim = grad_bound(*a) + torch.finfo(dtype).eps / 2 * np.abs(want) * (0 if dtype == torch.float32 else 1.01)
+        err = np.abs(got.double().cpu().numpy() - want)
+        assert (err <= lim).all(), (err / lim).max()
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_backward_against_differences(kind, renorm):
+    T, E, k, h = 6, 12, 3, 1e-6
+    l = logits_of(T, E, torch.float32, 77)
+    l64 = l.double().cpu().numpy()
+    idx = moe.moe_topk_route(l, k, score=SCORE[kind], dispatch=False)["idx"]
+    gw, gs = (torch.randn(s, generator=gen(5), device=DEV) for s in ((T, k), (T, E)))
+    got = moe.moe_topk_route_backward(l, idx, gw, score=SCORE[kind], renormalize=renorm, scale=2.0, grad_scores=gs)
+    i, w, s = idx.cpu().numpy(), gw.double().cpu().numpy(), gs.double().cpu().numpy()
+
+    def loss(x):
+        a, b = ref.weights_of(x, i, kind, renorm, 2.0)
+        return (a * w).sum(1) + (b * s).sum(1)
+
+    num = np.zeros((T, E))
+    for e in range(E):
+        d = np.zeros((1, E))
+        d[0, e] = h
+        num[:, e] = (loss(l64 + d) - loss(l64 - d)) / (2 * h)
+    # central differences: third derivatives below 10 times h^2, and 64-bit rounding of the loss over h
+    lim = 10 * h * h + 20 * 2.0 ** -52 / h + grad_bound(l64, i, w, kind, renorm, 2.0, s, T)
+    assert (np.abs(got.double().cpu().numpy() - num) <= lim).all()
+
+
+def test_route_backward_odd_indices():
+    # the same expert twice, and entries that are no expert
+    l = logits_of(4, 16, torch.float32, 9)
+    idx = torch.tensor([[3, 3, 5], [-1, 2, 16], [-5, -1, 1 << 30], [0, 15, 0]], dtype=torch.int32, device=DEV)
+    gw = torch.randn((4, 3), generator=gen(2), device=DEV)
+    for kind in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            got = moe.moe_topk_route_backward(l, idx, gw, score=SCORE[kind], renormalize=renorm)
+            a = (l.double().cpu().numpy(), idx.cpu().numpy().astype(np.int64), gw.double().cpu().numpy(), kind, renorm, 1.0)
+            want = ref.route_backward(*a)
+            assert (np.abs(got.double().cpu().numpy() - want) <= grad_bound(*a, None, 4)).all(), (kind, renorm)
+
+
+# ------------------------------------------------------------------- combine --
+
+@pytest.mark.parametrize("yt", [torch.float32, torch.bfloat16], ids=["yf32", "ybf16"])
+@pytest.mark.parametrize("ot", [torch.float32, torch.bfloat16], ids=["of32", "obf16"])
+@pytest.mark.parametrize("T,k,d", [(1, 1, 8), (3, 2, 1032), (17, 3, 6144), (40, 8, 64), (5, 32, 256)])
+@pytest.mark.parametrize("extras", [False, True])
+def test_combine(T, k, d, yt, ot, extras):
+    g = gen(T + k + d)
+    R = T * k + 3
+    y = torch.randn((R, d), generator=g, device=DEV).to(yt)
+    pos = torch.randint(0, R, (T, k), generator=g, device=DEV, dtype=torch.int32)
+    if extras:
+        pos[torch.rand((T, k), generator=g, device=DEV) < 0.2] = -1
+        pos[0, 0] = R                               # behind the last row
+        pos[T - 1] = -7                             # a token with nothing
+    y[R - 1] = float("nan")
+    pos[pos == R - 1] = 0                           # a row that no slot names stays unread
+    w = torch.rand((T, k), generator=g, device=DEV) if extras else None
+    res = torch.randn((T, d), generator=g, device=DEV).to(ot) if extras else None
+    got = moe.moe_combine_topk(y, pos, weights=w, residual=res, out_dtype=ot)
+    num = lambda t: None if t is None else t.double().cpu().numpy()  # noqa: E731
+    want, size = ref.combine(num(y), pos.cpu().numpy(), num(w), num(res))
+    # k products and k additions, one rounding each; then the output's own
+    lim = 2 * (k + 1) * U * size + torch.finfo(ot).eps / 2 * np.abs(want) * (0 if ot == torch.float32 else 1.01)
+    assert (np.abs(num(got) - want) <= lim + 1e-37).all()
+    if res is not None:                              # in place on the residual
+        again = moe.moe_combine_topk(y, pos, weights=w, residual=res, out=res)
+        assert again is res and torch.equal(res, got)
+
+
+def test_combine_agrees_with_moe_combine_bitwise():
+    from mixture_experts_ffn_14_b200 import expert_parallel as EP
+
+    T, d = 25, 96
+    y = torch.randn((2 * T, d), generator=gen(1), device=DEV)
+    pos = torch.randperm(2 * T, generator=gen(2), device=DEV).to(torch.int32).reshape(T, 2).contiguous()
+    comp = EP.LibraryCompute(None, torch.empty((1, 1, 1), device=DEV), None, None)
+    want = comp.combine({"T": T, "dtype": moe.MOE_BF16, "slot_pos": pos}, y)
+    assert torch.equal(moe.moe_combine_topk(y, pos, out_dtype=torch.bfloat16), want)
+
+
+def test_combine_no_rows():
+    out = moe.moe_combine_topk(torch.empty((0, 16), device=DEV), torch.zeros((3, 2), dtype=torch.int32, device=DEV))
+    assert torch.equal(out, torch.zeros((3, 16), device=DEV))
+
+
+# ------------------------------------------------------------ streams, graphs --
+
+def test_route_on_other_streams_and_in_graphs():
+    ls = [logits_of(T, 256, torch.bfloat16, T) for T in (300, 20)]
+    bias = torch.randn(256, generator=gen(1), device=DEV) * 0.05
+    kw = dict(score=moe.MOE_SCORE_SIGMOID, bias=bias, n_groups=8, topk_groups=4, group_rule=moe.MOE_GROUP_TOP2_SUM,
+              renormalize=True)
+    want = [moe.moe_topk_route(l, 8, **kw) for l in ls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[moe.moe_topk_route(l, 8, stream=s, **kw) for l, s in zip(ls, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for a, b in zip(pair, want):
+            assert all(torch.equal(a[n], b[n]) for n in b)
+    nt = torch.tensor([300], dtype=torch.int32, device=DEV)
+    static = ls[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = moe.moe_topk_route(static, 8, n_tokens=nt, **kw)
+        back = moe.moe_topk_route_backward(static, r["idx"], r["weights"], score=moe.MOE_SCORE_SIGMOID, renormalize=True,
+                                           n_tokens=nt)
+    for n, seed in ((300, 1), (7, 2), (0, 3), (299, 4)):
+        static.copy_(logits_of(300, 256, torch.bfloat16, seed))
+        nt.fill_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(r, static, 8, "sigmoid", bias, 8, 4, "top2", True, 1.0, n)
+        assert (back[n:] == 0).all() and bool(torch.isfinite(back).all())
