@@ -83,11 +83,12 @@ typedef enum {
 typedef enum {
   MOE_F32 = 0,         /* fp32 activations and weights, fp32 arithmetic        */
   MOE_BF16 = 1,        /* bf16 activations and weights, fp32 accumulation      */
-  MOE_BF16_INT8W = 2   /* bf16 activations, int8 weights + bf16 channel scales;
+  MOE_BF16_INT8W = 2,  /* bf16 activations, int8 weights + bf16 channel scales;
                           the expert GEMMs run on fp16 operands: int8 -> fp16 is
                           exact, bf16 activations -> fp16 is exact for normal
                           values below 65504 in magnitude, and the GeGLU
                           intermediate is kept in fp16 (range |h| < 65504)     */
+  MOE_INT8 = 3         /* rows that are 8-bit integers already (moe_int8_product) */
 } moe_dtype_t;
 
 /* Activation on the gate branch of every expert. */
@@ -306,10 +307,12 @@ MOE_EXPORT moe_status_t moe_gather_rows(const void* src, int64_t src_rows, const
                                         int64_t row_bytes, void* dst, void* workspace, size_t ws_bytes,
                                         moe_stream_t stream);
 
-/* ---- Routing and combine of any E and k -------------------------------------
+/* ---- Routing, products and combine of any E and k ---------------------------
  * The sublayer above fixes E = 8, k = 2 and the softmax router. The calls below
- * route and combine for other routers, and give the router's gradient for
- * training. They follow the file header's rules
+ * make the same layer of other routers and of 8-bit arithmetic:
+ *   moe_topk_route -> moe_int8_product (gate/up) -> moe_int8_product (down)
+ *   -> moe_combine_topk
+ * and give the router's gradient for training. They follow the file header's rules
  * (dense, row-major, 16-byte aligned device arrays; checks on the host; no
  * synchronisation; nothing kept between calls); calls that may overlap on the
  * GPU need distinct workspaces and outputs. */
@@ -385,6 +388,48 @@ MOE_EXPORT moe_status_t moe_topk_route_backward(const moe_topk_args_t* args,
                                                 const float* grad_scores,    /* [T, E] or NULL       */
                                                 void* grad_logits,           /* [T, E], logits' type */
                                                 moe_stream_t stream);
+
+/* Product of rows and int8 weights in 8-bit integers, one scale per row and one
+ * per output channel, rows grouped by expert (or one plain matrix):
+ *   y[r, n] = gate[r] * a[r] * s[e, n] * sum_k q[r, k] * w[e, k, n]
+ * the sum in 32-bit integers (exact). With w_up the call computes the gated pair
+ * of an expert, y = gate * act(z_w) * z_w_up, in one kernel. x in 16 or 32 bits
+ * is brought to 8 on the way: a[r] = max|x[r]| / 127, q = x / a rounded to nearest
+ * (ties to even; decided exactly), a row of zeros staying zero and a row with an
+ * infinity or NaN giving a row of NaN; `index` gathers its rows.
+ * w, w_up [n_experts, K, N] int8 and s, s_up [n_experts, N] bf16 are laid out as the
+ * weights and scales of MOE_BF16_INT8W.
+ * Limits: 0 <= R <= 2^24, K and N multiples of 16, 16 <= K < 131072 (the sum stays
+ * below 2^31), 16 <= N <= 2^20, 1 <= n_experts <= 1024. */
+typedef struct {
+  const void* x;          /* [x_rows, K] MOE_F32 / MOE_BF16, or [R, K] MOE_INT8             */
+  const float* x_scale;   /* [R]: MOE_INT8 rows' scales; else NULL                          */
+  const int32_t* index;   /* [R] row of x for each row, or NULL (x_rows == R); an entry outside
+                             [0, x_rows) stands for a row of zeros; NULL with MOE_INT8       */
+  const int32_t* counts;  /* [n_experts] rows of each expert, in order (device); NULL with
+                             n_experts == 1: all R rows. Rows of out behind the last expert's
+                             are left as they were                                          */
+  const void* w;          /* [n_experts, K, N] int8                                         */
+  const void* w_up;       /* the same, or NULL                                              */
+  const void* s;          /* [n_experts, N] bf16                                            */
+  const void* s_up;       /* the same with w_up, else NULL                                  */
+  const float* gate;      /* [R] or NULL for 1                                              */
+  void* out;              /* [R, N] MOE_F32 or MOE_BF16                                     */
+  int64_t x_rows, R, K, N;
+  int32_t n_experts;
+  moe_dtype_t x_dtype, out_dtype;
+  moe_activation_t activation; /* with w_up                                                  */
+} moe_int8_args_t;
+
+/* Workspace bytes of moe_int8_product, 0 on bad sizes or R == 0. 256-byte multiple. */
+MOE_EXPORT size_t moe_int8_workspace_size(int64_t R, int64_t K, int64_t N, int32_t n_experts,
+                                          moe_dtype_t x_dtype, int32_t with_up);
+
+/* See moe_int8_args_t. The status word at the start of the workspace also gets bit
+ * 0x40 (in every build) when counts hold a negative number or add up to more than R:
+ * such rows are not computed. */
+MOE_EXPORT moe_status_t moe_int8_product(const moe_int8_args_t* args, void* workspace, size_t ws_bytes,
+                                         moe_stream_t stream);
 
 /* out[t] = residual[t] + sum over the k slots of weights[t, s] * y[slot_pos[t, s]],
  * summed in fp32 in slot order and rounded once. y [R, d] and out [T, d] are MOE_F32

@@ -15,9 +15,10 @@ import ctypes
 from . import _native as N
 from ._native import (  # noqa: F401
     MOE_ACT_GELU_ERF, MOE_ACT_GELU_TANH, MOE_ACT_SILU, MOE_BF16, MOE_BF16_INT8W, MOE_F32, MOE_GROUP_MAX,
-    MOE_GROUP_TOP2_SUM, MOE_PATH_AUTO, MOE_PATH_TOKEN_TILE, MOE_PATH_TOKEN_TILE_SINGLE, MOE_PATH_WEIGHT_STREAM,
-    MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX,
+    MOE_GROUP_TOP2_SUM, MOE_INT8, MOE_PATH_AUTO, MOE_PATH_TOKEN_TILE, MOE_PATH_TOKEN_TILE_SINGLE,
+    MOE_PATH_WEIGHT_STREAM, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX,
 )
+from .int8 import moe_int8_product, moe_int8_workspace_size  # noqa: F401
 from .routed import (  # noqa: F401
     moe_combine_topk, moe_topk_route, moe_topk_route_backward, moe_topk_workspace_size,
 )
@@ -25,7 +26,8 @@ from .routed import (  # noqa: F401
 __all__ = ["MoeError", "moe_forward", "moe_forward_ex", "moe_forward_noalloc", "moe_workspace_size",
            "moe_workspace_size_ex", "moe_build_flags",
            "moe_device_status", "moe_selftest_bounded_wait", "moe_status_string", "moe_abi_version",
-           "dtype_code", "moe_topk_route", "moe_topk_route_backward", "moe_topk_workspace_size", "moe_combine_topk"]
+           "dtype_code", "moe_topk_route", "moe_topk_route_backward", "moe_topk_workspace_size", "moe_combine_topk",
+           "moe_int8_product", "moe_int8_workspace_size"]
 
 
 class MoeError(RuntimeError):

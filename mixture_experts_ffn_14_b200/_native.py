@@ -21,7 +21,7 @@ MOE_BUILD_DEBUG_BOUNDS = 1
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_MISALIGNED = 0, 1, 2, 3
 MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE_CHECK = 4, 5, 6
-MOE_F32, MOE_BF16, MOE_BF16_INT8W = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_BF16_INT8W, MOE_INT8 = 0, 1, 2, 3
 MOE_ACT_GELU_TANH, MOE_ACT_GELU_ERF, MOE_ACT_SILU = 0, 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_GROUP_MAX, MOE_GROUP_TOP2_SUM = 0, 1
@@ -78,6 +78,13 @@ class MoeTopkRouted(ctypes.Structure):
                 ("gate_perm", c_void_p)]
 
 
+class MoeInt8Args(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("x_scale", c_void_p), ("index", c_void_p), ("counts", c_void_p), ("w", c_void_p),
+                ("w_up", c_void_p), ("s", c_void_p), ("s_up", c_void_p), ("gate", c_void_p), ("out", c_void_p),
+                ("x_rows", c_int64), ("R", c_int64), ("K", c_int64), ("N", c_int64), ("n_experts", c_int32),
+                ("x_dtype", c_int), ("out_dtype", c_int), ("activation", c_int)]
+
+
 EXPORTS.update({
     "moe_forward": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, POINTER(MoeScales), c_void_p,
                             c_int64, c_int64, c_int64, c_int32, c_int32, c_int, c_void_p]),
@@ -103,6 +110,8 @@ EXPORTS.update({
     "moe_topk_workspace_size": (c_size_t, [c_int64, c_int32, c_int32]),
     "moe_topk_route": (c_int, [POINTER(MoeTopkArgs), POINTER(MoeTopkRouted), c_void_p, c_size_t, c_void_p]),
     "moe_topk_route_backward": (c_int, [POINTER(MoeTopkArgs), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_int8_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32, c_int, c_int32]),
+    "moe_int8_product": (c_int, [POINTER(MoeInt8Args), c_void_p, c_size_t, c_void_p]),
     "moe_combine_topk": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_void_p, c_int64, c_int32, c_int64, c_void_p,
                                  c_void_p, c_int, c_void_p]),
 })

@@ -1,0 +1,729 @@
+// gemm_int8.cu — products of rows and int8 weights in 8-bit integers with a scale
+// per row and per output channel (moe_int8_product), rows grouped by expert.
+//
+//   y[r, n] = gate[r] * a[r] * s[e, n] * sum_k q[r, k] * w[e, k, n]
+//   gated pair: y = gate * act(z_w) * z_w_up, both products in one kernel
+//
+// The sums run on the 5th-generation tensor cores as kind::i8 (signed 8-bit operands,
+// 32-bit integer sums, exact for K < 2^17), at twice the 16-bit rate and on half the
+// bytes of the 16-bit forms. The weights are read in the caller's [E, K, N] layout as
+// the MN-major operand (one TMA box = 128 K rows of 128 columns, 128-B swizzle), the
+// rows as the K-major one.
+//
+// Launches: a prepare kernel (row scales and quantised rows, tile schedule), then
+// the product kernel.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "gemm_common.cuh"
+
+namespace moe {
+namespace i8 {
+
+using namespace moe::sm100;
+using tc::kWaitLimitNs;
+using tc::pack_bf16x2;
+using tc::warp_wait;
+
+constexpr int BK = 128;              // K per stage: 128 bytes = one swizzle row
+constexpr int WBOX = BK * 128;       // 16 KB: [128 K x 128 columns]
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxCtas = 160;        // product CTAs at most (workspace sizing; 148 SMs on B200)
+
+// Tile schedule in the workspace, made by the prepare kernel.
+struct Sched {
+  int32_t cnt[kMaxExperts];      // rows of each expert
+  int32_t off[kMaxExperts];      // first row
+  int32_t pre[kMaxExperts + 1];  // row tiles before each expert
+};
+
+// ---------------------------------------------------------------- prepare --
+
+struct PrepParams {
+  const void* x;
+  const int32_t* index;
+  const int32_t* counts;
+  int64_t x_rows, R, K;
+  int32_t n_experts, tile_rows;
+  bool quantise;
+  int8_t* q;       // [R, K]
+  float* a;        // [R]
+  Sched* sched;
+  int32_t* counters;  // [kMaxCtas] zeroed
+  uint32_t* status;
+};
+
+constexpr int kPrepThreads = 256;
+
+// Prefix sums of the experts' rows and row tiles by one CTA. Counts that are
+// negative or run past R are cut off (status bit kStatusBounds), so that no row
+// outside [0, R) is ever touched.
+__device__ void make_schedule(const PrepParams& p) {
+  constexpr int PER = kMaxExperts / kPrepThreads;
+  __shared__ long long part_rows[kPrepThreads / 32];
+  __shared__ int part_tiles[kPrepThreads / 32];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  for (int i = tid; i < kMaxCtas; i += kPrepThreads) p.counters[i] = 0;
+  long long c[PER], rows = 0;
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int e = tid * PER + j;
+    c[j] = 0;
+    if (e < p.n_experts) c[j] = p.counts != nullptr ? p.counts[e] : p.R;
+    if (c[j] < 0) {
+      c[j] = 0;
+      bad = true;
+    }
+    rows += c[j];
+  }
+  long long inc = rows;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) part_rows[warp] = inc;
+  __syncthreads();
+  long long at = inc - rows;
+  for (int w = 0; w < warp; ++w) at += part_rows[w];
+  int tiles = 0, mine[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int e = tid * PER + j;
+    const long long left = at < p.R ? p.R - at : 0;
+    const int cut = static_cast<int>(c[j] < left ? c[j] : left);
+    if (cut < c[j]) bad = true;
+    if (e < p.n_experts) {
+      p.sched->cnt[e] = cut;
+      p.sched->off[e] = static_cast<int32_t>(at < p.R ? at : p.R);
+    }
+    at += c[j];
+    mine[j] = (cut + p.tile_rows - 1) / p.tile_rows;
+    tiles += mine[j];
+  }
+  int tinc = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, tinc, o);
+    if (lane >= o) tinc += v;
+  }
+  if (lane == 31) part_tiles[warp] = tinc;
+  __syncthreads();
+  int t = tinc - tiles;
+  for (int w = 0; w < warp; ++w) t += part_tiles[w];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int e = tid * PER + j;
+    if (e < p.n_experts) p.sched->pre[e] = t;
+    t += mine[j];
+    if (e == p.n_experts - 1) p.sched->pre[p.n_experts] = t;
+  }
+  const int any = __syncthreads_or(bad);
+  if (tid == 0) *p.status = any ? kStatusBounds : 0u;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* row, int64_t v, float (&f)[8]) {
+  if (BF16) {
+    const uint4 u = static_cast<const uint4*>(row)[v];
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = __uint_as_float(w[j] << 16);
+      f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  } else {
+    const float4 a = static_cast<const float4*>(row)[2 * v], b = static_cast<const float4*>(row)[2 * v + 1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+}
+
+// x / (top / 127) rounded to nearest, ties to even, as the exact quotient rounds.
+// The fp32 quotient is off by at most 127 * 2 * 2^-24 < 2e-5; one further than 1e-4
+// from a half rounds as the exact one does, the others (and those whose reciprocal
+// left the fp32 range) are divided in 64 bits, where 127 x is exact and no quotient
+// of two fp32 numbers is nearer to a half than 2^-33 without being one.
+__device__ __forceinline__ int quantise(float x, float r, float top) {
+  const float y = x * r;
+  float q = rintf(y);
+  if (!(fabsf(fabsf(y - q) - 0.5f) >= 1e-4f)) q = static_cast<float>(rint(127.0 * x / top));
+  return static_cast<int>(q);
+}
+
+// One row per CTA: its largest magnitude (as bits, so that NaN and infinity win), then
+// the quotients. Rows of up to kPrepThreads * 8 * MAXV values stay in registers
+// between the two passes; longer ones (MAXV = 0) are read again, from L2.
+template <bool BF16, int MAXV>
+__global__ void __launch_bounds__(kPrepThreads) moe_int8_prepare_kernel(const __grid_constant__ PrepParams p) {
+  if (blockIdx.x == 0) {
+    make_schedule(p);
+    return;
+  }
+  __shared__ uint32_t part[kPrepThreads / 32];
+  const int64_t r = static_cast<int64_t>(blockIdx.x) - 1;
+  const int64_t src = p.index != nullptr ? p.index[r] : r;
+  const bool real = src >= 0 && src < p.x_rows;
+  const int nvec = static_cast<int>(p.K / 8);
+  const void* row = static_cast<const uint8_t*>(p.x) + (real ? src : 0) * p.K * (BF16 ? 2 : 4);
+  constexpr int KEEP = MAXV > 0 ? MAXV : 1;
+  float f[KEEP][8];
+  uint32_t top_bits = 0;
+  if (real) {
+    if (MAXV > 0) {
+#pragma unroll
+      for (int i = 0; i < KEEP; ++i) {
+        const int v = threadIdx.x + i * kPrepThreads;
+        if (v < nvec) load8<BF16>(row, v, f[i]);
+      }
+    }
+    for (int i = 0; i * kPrepThreads < nvec; ++i) {
+      const int v = threadIdx.x + i * kPrepThreads;
+      if (MAXV == 0) {
+        if (v < nvec) load8<BF16>(row, v, f[0]);
+      } else if (i > 0) {
+        break;
+      }
+#pragma unroll
+      for (int m = 0; m < KEEP; ++m)
+        if (v + m * kPrepThreads < nvec && (MAXV > 0 || m == 0)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top_bits = max(top_bits, __float_as_uint(f[m][j]) & 0x7fffffffu);
+        }
+    }
+  }
+  top_bits = __reduce_max_sync(0xffffffffu, top_bits);
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top_bits;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kPrepThreads / 32; ++w) top_bits = max(top_bits, part[w]);
+  const float top = __uint_as_float(top_bits);
+  const bool finite = top_bits < 0x7f800000u;
+  const bool zero = !finite || top_bits == 0;  // q = 0; a = NaN or 0
+  const float rcp = zero ? 0.0f : 127.0f / top;
+  if (threadIdx.x == 0) p.a[r] = finite ? top / 127.0f : __uint_as_float(0x7fc00000u);
+  uint2* dst = reinterpret_cast<uint2*>(p.q + r * p.K);
+  auto emit = [&](int v, const float (&g)[8]) {
+    uint32_t w[2] = {0, 0};
+    if (!zero) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        w[j / 4] |= static_cast<uint32_t>(quantise(g[j], rcp, top) & 0xff) << (8 * (j % 4));
+    }
+    dst[v] = make_uint2(w[0], w[1]);
+  };
+  if (MAXV > 0) {
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) {
+      const int v = threadIdx.x + i * kPrepThreads;
+      if (v < nvec) emit(v, f[i]);
+    }
+  } else {
+    for (int v = threadIdx.x; v < nvec; v += kPrepThreads) {
+      if (real) load8<BF16>(row, v, f[0]);
+      emit(v, f[0]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- product --
+
+struct Params {
+  const Sched* sched;
+  const float* a;        // [R] row scales
+  const float* gate;     // [R] or nullptr
+  const __nv_bfloat16* s0;
+  const __nv_bfloat16* s1;
+  void* out;
+  int32_t* counters;     // stream form: K blocks summed of a tile that several CTAs share
+  int32_t* part;         // stream form: their partial sums
+  uint32_t* status;
+  int64_t R;
+  int32_t N, n_experts, nt, kb, act;
+};
+
+// Gate activation in fp32: z * sigmoid(.) forms, which keep the relative accuracy
+// of large negative z (1 + tanh would cancel); the approximate exponential and
+// quotient are off by about 2^-21, below the rounding of either output type's sums.
+__device__ __forceinline__ float act_f32(float z, int mode) {
+  if (mode == MOE_ACT_GELU_ERF) return 0.5f * z * erfcf(-0.70710678118654752f * z);
+  const float t = mode == MOE_ACT_SILU ? z : 1.5957691216057308f * (z + 0.044715f * z * z * z);
+  return __fdividef(z, 1.0f + __expf(-t));
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Index of the expert that holds row tile `m` (pre[e] <= m < pre[e + 1]).
+__device__ __forceinline__ int expert_of(const int32_t* pre, int n, int m) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (pre[mid] <= m) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// ---- stream form ----------------------------------------------------------
+// For few rows per expert: the weights' columns are the MMA's M side and the tile's
+// tokens (at most ROWS) its N side, so the tensor work follows the tokens there are
+// and the kernel is bound by reading each weight byte once. All CTAs take equal runs
+// of the (tile, K block) sequence; a tile that the runs cut is summed from its parts:
+// every CTA but the one that brings the last part stores its 32-bit sums and counts
+// its K blocks, that one adds all parts (integers: any order gives the same sum) and
+// finishes the tile. No CTA waits for another.
+
+template <int ROWS>
+struct StreamCfg {
+  static constexpr int X_BYTES = ROWS * BK;
+  static constexpr int STAGE_BYTES = X_BYTES + 2 * WBOX;
+  static constexpr int STAGES = ROWS <= 64 ? 5 : 4;
+  static constexpr int ACC_COLS = 2 * ROWS;  // two 128-column blocks of weights
+  static constexpr int TMEM_COLS = 2 * ACC_COLS;
+  static constexpr int PART_INTS = 256 * ROWS;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 256;  // alignment slack, barriers; + schedule
+};
+constexpr int XBOX_ROWS = 32;
+constexpr int kMinRun = 2;
+
+struct Seg {
+  int e, row0, rows, n0, kb0, kb1;
+  int64_t tile0;  // first K block of the tile in the whole sequence
+};
+
+template <int ROWS, bool DUAL, bool OB>
+__global__ void __launch_bounds__(256, 1)
+    moe_int8_stream_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
+                           const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ Params p) {
+  using C = StreamCfg<ROWS>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES);
+  uint64_t* empty_bar = full_bar + C::STAGES;
+  uint64_t* tfull_bar = empty_bar + C::STAGES;
+  uint64_t* tempty_bar = tfull_bar + 2;
+  uint64_t* drain_bar = tempty_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* last_flag = abort_flag + 1;
+  int32_t* pre = reinterpret_cast<int32_t*>(full_bar) + 64;  // 256 B after the barriers' start
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull_bar[b], 1);
+      mbar_init(&tempty_bar[b], 4);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_w0);
+    if (DUAL) tma_prefetch_desc(&tm_w1);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  for (int e = threadIdx.x; e <= p.n_experts; e += 256) pre[e] = p.sched->pre[e];
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int64_t total = static_cast<int64_t>(pre[p.n_experts]) * p.nt * p.kb;
+  // Runs of at least kMinRun K blocks: no run is empty, and the last CTAs of a small
+  // problem have nothing to do.
+  const int64_t G = min(static_cast<int64_t>(gridDim.x), max(total / kMinRun, int64_t(1)));
+  const int64_t me = blockIdx.x;
+  const int64_t lo = me < G ? total * me / G : total, hi = me < G ? total * (me + 1) / G : total;
+
+  // The part of this CTA's run that starts at `pos`: one tile or a piece of it.
+  // Row tiles run fastest within an expert, so tiles that share weights follow
+  // one another.
+  auto segment = [&](int64_t pos, Seg& s) {
+    const int64_t tile = pos / p.kb;
+    s.tile0 = tile * p.kb;
+    s.kb0 = static_cast<int>(pos - s.tile0);
+    const int64_t end = hi - s.tile0;
+    s.kb1 = static_cast<int>(end < p.kb ? end : p.kb);
+    s.e = expert_of(pre, p.n_experts, static_cast<int>(tile / p.nt));
+    const int mt = pre[s.e + 1] - pre[s.e];
+    const int local = static_cast<int>(tile - static_cast<int64_t>(pre[s.e]) * p.nt);
+    const int m = local % mt;
+    s.n0 = (local / mt) * (DUAL ? 128 : 256);
+    const int cnt = p.sched->cnt[s.e];
+    s.row0 = p.sched->off[s.e] + m * ROWS;
+    s.rows = min(ROWS, cnt - m * ROWS);
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ producer --
+    const uint64_t wpolicy = policy_evict_first();
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    Seg s;
+    for (int64_t pos = lo; ok && pos < hi; pos = s.tile0 + s.kb1) {
+      segment(pos, s);
+      const int boxes = (s.rows + XBOX_ROWS - 1) / XBOX_ROWS;
+      for (int kb = s.kb0; kb < s.kb1; ++kb) {
+        if (!mbar_wait(&empty_bar[stage], phase ^ 1, kWaitLimitNs) || *abort_flag) {
+          atomicOr(p.status, kStatusProducerTimeout);
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        uint8_t* xs = smem + stage * C::STAGE_BYTES;
+        uint8_t* ws = xs + C::X_BYTES;
+        mbar_arrive_expect_tx(&full_bar[stage], boxes * XBOX_ROWS * BK + 2 * WBOX);
+        tma_load_3d_hint(ws, &tm_w0, &full_bar[stage], s.n0, kb * BK, s.e, wpolicy);
+        tma_load_3d_hint(ws + WBOX, DUAL ? &tm_w1 : &tm_w0, &full_bar[stage], DUAL ? s.n0 : s.n0 + 128, kb * BK,
+                         s.e, wpolicy);
+        for (int b = 0; b < boxes; ++b)
+          tma_load_2d(xs + b * XBOX_ROWS * BK, &tm_x, &full_bar[stage], kb * BK, s.row0 + b * XBOX_ROWS);
+        ++issued;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok) {  // unwinding: no copy may still be on its way into this CTA's memory
+      for (int i = 0; i < min(issued, C::STAGES); ++i) {
+        if (--stage < 0) {
+          stage = C::STAGES - 1;
+          phase ^= 1;
+        }
+        mbar_wait(&full_bar[stage], phase, kWaitLimitNs);
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    // ----------------------------------------------------------------- MMA --
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    Seg s;
+    for (int64_t pos = lo; ok && pos < hi; pos = s.tile0 + s.kb1) {
+      segment(pos, s);
+      if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1, kWaitLimitNs) || *abort_flag) ok = false;
+      tc_fence_after();
+      const uint32_t d = tmem_base + acc * C::ACC_COLS;
+      const uint32_t ntok = (s.rows + 31) / 32 * 32;
+      const uint32_t idesc = idesc_s8_s32(128, ntok, 1, 0);
+      for (int kb = s.kb0; ok && kb < s.kb1; ++kb) {
+        if (!mbar_wait(&full_bar[stage], phase, kWaitLimitNs) || *abort_flag) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t xs = smem_u32(smem + stage * C::STAGE_BYTES);
+        const uint32_t ws = xs + C::X_BYTES;
+#pragma unroll
+        for (int k = 0; k < BK / 32; ++k) {
+          // Weights: MN-major, 128 columns to a swizzle row, 8-deep K groups 1024 B
+          // apart; a 32-deep step is 4096 B. Tokens: K-major, 8-row groups 1024 B
+          // apart; the step is 32 B inside the swizzled row.
+          const uint32_t accum = kb > s.kb0 || k > 0;
+          const uint64_t xd = smem_desc_sw128(xs + k * 32, 16, 1024);
+          umma_s8(d, smem_desc_sw128(ws + k * 4096, WBOX, 1024), xd, idesc, accum);
+          umma_s8(d + ROWS, smem_desc_sw128(ws + WBOX + k * 4096, WBOX, 1024), xd, idesc, accum);
+        }
+        umma_commit(&empty_bar[stage]);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (ok) umma_commit(&tfull_bar[acc]);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+    if (!ok) {
+      atomicOr(p.status, kStatusMmaTimeout);
+      *abort_flag = 1;
+      umma_commit(drain_bar);  // unwinding: the tensor cores are done before TMEM is freed
+      mbar_wait(drain_bar, 0, kWaitLimitNs);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue --
+    // Lane = weight column 32 q + lane of each of the two blocks.
+    const int q = warp - 4, col = 32 * q + lane;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    Seg s;
+    for (int64_t pos = lo; pos < hi; pos = s.tile0 + s.kb1) {
+      segment(pos, s);
+      if (!warp_wait(&tfull_bar[acc], acc_phase, abort_flag)) {
+        atomicOr(p.status, kStatusEpilogueTimeout);
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * C::ACC_COLS;
+      const bool whole = s.kb1 - s.kb0 == p.kb;
+      // Parts of the tile: CTAs first .. last hold its K blocks; the first one's part
+      // is the end of its run (slot 1), the others' the start of theirs (slot 0).
+      int first = 0, last = 0;
+      bool finish = true;
+      if (!whole) {
+        first = static_cast<int>(((s.tile0 + 1) * G - 1) / total);
+        last = static_cast<int>(((s.tile0 + p.kb) * G - 1) / total);
+        int32_t* mine = p.part + (2 * me + (me == first ? 1 : 0)) * C::PART_INTS;
+#pragma unroll 1
+        for (int j0 = 0; j0 < s.rows; j0 += 16) {
+          uint32_t u[16], v[16];
+          tmem_ld16x2(tb + j0, tb + ROWS + j0, u, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j0 + j < s.rows) {
+              __stcg(mine + (j0 + j) * 256 + col, static_cast<int>(u[j]));
+              __stcg(mine + (j0 + j) * 256 + 128 + col, static_cast<int>(v[j]));
+            }
+        }
+        __threadfence();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (threadIdx.x == 128) {
+          const int had = tc::atomic_add_acq_rel_gpu(&p.counters[first], s.kb1 - s.kb0);
+          *last_flag = had + (s.kb1 - s.kb0) == p.kb;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        finish = *last_flag != 0;
+        if (finish) __threadfence();
+      }
+      if (finish) {
+        const int ca = s.n0 + col, cb = DUAL ? ca : ca + 128;
+        const bool va = ca < p.N, vb = cb < p.N;
+        const int64_t se = static_cast<int64_t>(s.e) * p.N;
+        const float sa = va ? __bfloat162float(p.s0[se + ca]) : 0.0f;
+        const float sb = vb ? __bfloat162float((DUAL ? p.s1 : p.s0)[se + cb]) : 0.0f;
+#pragma unroll 1
+        for (int j0 = 0; j0 < s.rows; j0 += 16) {
+          uint32_t u[16], v[16];
+          tmem_ld16x2(tb + j0, tb + ROWS + j0, u, v);
+          if (!whole) {
+            for (int c = first; c <= last; ++c) {
+              if (c == me) continue;
+              const int32_t* o = p.part + (2 * static_cast<int64_t>(c) + (c == first ? 1 : 0)) * C::PART_INTS;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (j0 + j < s.rows) {
+                  u[j] += static_cast<uint32_t>(__ldcg(o + (j0 + j) * 256 + col));
+                  v[j] += static_cast<uint32_t>(__ldcg(o + (j0 + j) * 256 + 128 + col));
+                }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (j0 + j >= s.rows) continue;
+            const int64_t row = s.row0 + j0 + j;
+            const float a = __ldg(p.a + row), g = p.gate != nullptr ? __ldg(p.gate + row) : 1.0f;
+            const float za = static_cast<float>(static_cast<int>(u[j])) * a * sa;
+            const float zb = static_cast<float>(static_cast<int>(v[j])) * a * sb;
+            auto put = [&](int c, float y) {
+              if (OB) static_cast<__nv_bfloat16*>(p.out)[row * p.N + c] = __float2bfloat16_rn(y);
+              else static_cast<float*>(p.out)[row * p.N + c] = y;
+            };
+            if (DUAL) {
+              if (va) put(ca, act_f32(za, p.act) * zb * g);
+            } else {
+              if (va) put(ca, za * g);
+              if (vb) put(cb, zb * g);
+            }
+          }
+        }
+      }
+      if (!whole) asm volatile("bar.sync 1, 128;" ::: "memory");  // last_flag read by all before the next one
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty_bar[acc]);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------- host --
+
+struct Layout {
+  size_t status, sched, counters, q, a, part, total;
+  int32_t tile_rows;  // rows of a tile: 64 or 128 (stream form)
+};
+
+Layout plan(int64_t R, int64_t K, int32_t n_experts, moe_dtype_t x_dtype) {
+  Layout L{};
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = (o + bytes + 255) / 256 * 256;
+    return at;
+  };
+  L.tile_rows = R <= 48 * static_cast<int64_t>(n_experts) ? 64 : 128;
+  L.status = take(256);
+  L.sched = take(sizeof(Sched));
+  L.counters = take(sizeof(int32_t) * kMaxCtas);
+  if (x_dtype != MOE_INT8) {
+    L.q = take(static_cast<size_t>(R) * K);
+    L.a = take(sizeof(float) * R);
+  }
+  L.part = take(sizeof(int32_t) * 2 * kMaxCtas * 256 * static_cast<size_t>(L.tile_rows));
+  L.total = o;
+  return L;
+}
+
+moe_status_t check_sizes(int64_t R, int64_t K, int64_t N, int32_t n_experts, moe_dtype_t x_dtype) {
+  if (R < 0 || K <= 0 || N <= 0 || n_experts < 1) return MOE_ERR_INVALID_ARG;
+  if (x_dtype != MOE_F32 && x_dtype != MOE_BF16 && x_dtype != MOE_INT8) return MOE_ERR_INVALID_ARG;
+  if (K % 16 != 0 || N % 16 != 0 || K >= 131072 || N > (int64_t(1) << 20) || R > (int64_t(1) << 24) ||
+      n_experts > kMaxExperts)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool weight_map(CUtensorMap* m, const void* w, const moe_int8_args_t* a) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(a->N), static_cast<uint64_t>(a->K),
+                            static_cast<uint64_t>(a->n_experts)};
+  const uint64_t strides[2] = {dims[0], dims[0] * dims[1]};
+  const uint32_t box[3] = {128, BK, 1};
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, w, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool row_map(CUtensorMap* m, const void* q, const moe_int8_args_t* a, uint32_t box_rows) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(a->K), static_cast<uint64_t>(a->R)};
+  const uint64_t strides[1] = {dims[0]};
+  const uint32_t box[2] = {BK, box_rows};
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int ROWS, bool DUAL, bool OB>
+cudaError_t launch_stream(const moe_int8_args_t* a, const void* q, Params p, cudaStream_t s) {
+  using C = StreamCfg<ROWS>;
+  auto kern = moe_int8_stream_kernel<ROWS, DUAL, OB>;
+  constexpr int kSmem = C::SMEM + (kMaxExperts + 1) * 4;
+  static_assert(kSmem <= 232448, "shared memory above the per-block limit");
+  static_assert((2 * C::STAGES + 5) * 8 + 16 <= 256, "barrier area too small");
+  const cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), kSmem);
+  if (err != cudaSuccess) return err;
+  CUtensorMap tx, tw0, tw1;
+  if (!row_map(&tx, q, a, XBOX_ROWS) || !weight_map(&tw0, a->w, a) || !weight_map(&tw1, DUAL ? a->w_up : a->w, a))
+    return cudaErrorInvalidValue;
+  p.nt = static_cast<int32_t>((a->N + (DUAL ? 127 : 255)) / (DUAL ? 128 : 256));
+  const int64_t most = ((a->R + ROWS - 1) / ROWS + a->n_experts) * p.nt * p.kb;
+  const int grid = static_cast<int>(std::min<int64_t>(std::min(device_sm_count(), kMaxCtas), most));
+  kern<<<grid, 256, kSmem, s>>>(tx, tw0, tw1, p);
+  return cudaGetLastError();
+}
+
+template <bool BF16>
+cudaError_t launch_prepare(const PrepParams& p, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(1 + (p.quantise ? p.R : 0));
+  const int64_t vec = (p.K / 8 + kPrepThreads - 1) / kPrepThreads;  // 8-value vectors per thread
+  if (vec <= 1) moe_int8_prepare_kernel<BF16, 1><<<grid, kPrepThreads, 0, s>>>(p);
+  else if (vec <= 4) moe_int8_prepare_kernel<BF16, 4><<<grid, kPrepThreads, 0, s>>>(p);
+  else if (vec <= 16) moe_int8_prepare_kernel<BF16, 16><<<grid, kPrepThreads, 0, s>>>(p);
+  else moe_int8_prepare_kernel<BF16, 0><<<grid, kPrepThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace i8
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_int8_workspace_size(int64_t R, int64_t K, int64_t N, int32_t n_experts, moe_dtype_t x_dtype,
+                               int32_t with_up) {
+  if (R <= 0 || (with_up != 0 && with_up != 1) || i8::check_sizes(R, K, N, n_experts, x_dtype) != MOE_OK) return 0;
+  return i8::plan(R, K, n_experts, x_dtype).total;
+}
+
+moe_status_t moe_int8_product(const moe_int8_args_t* a, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+  if (!a) return MOE_ERR_INVALID_ARG;
+  const moe_status_t st = i8::check_sizes(a->R, a->K, a->N, a->n_experts, a->x_dtype);
+  if (st != MOE_OK) return st;
+  if (a->out_dtype != MOE_F32 && a->out_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  const bool rows8 = a->x_dtype == MOE_INT8, dual = a->w_up != nullptr;
+  if (dual && (a->activation < MOE_ACT_GELU_TANH || a->activation > MOE_ACT_SILU)) return MOE_ERR_INVALID_ARG;
+  if (a->x_rows < 0 || a->x_rows > (int64_t(1) << 31) || (!a->index && a->x_rows != a->R)) return MOE_ERR_INVALID_ARG;
+  if (a->R == 0) return MOE_OK;
+  if ((!a->x && a->x_rows > 0) || !a->w || !a->s || !a->out || (dual != (a->s_up != nullptr))) return MOE_ERR_INVALID_ARG;
+  if (rows8 != (a->x_scale != nullptr) || (rows8 && a->index) || (!a->counts && a->n_experts != 1))
+    return MOE_ERR_INVALID_ARG;
+  const void* const all[] = {a->x, a->x_scale, a->index, a->counts, a->w, a->w_up, a->s, a->s_up, a->gate, a->out};
+  for (const void* q : all)
+    if (!i8::aligned16(q)) return MOE_ERR_MISALIGNED;
+  const i8::Layout L = i8::plan(a->R, a->K, a->n_experts, a->x_dtype);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < L.total)
+    return MOE_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+  i8::PrepParams pp{};
+  pp.x = a->x;
+  pp.index = a->index;
+  pp.counts = a->counts;
+  pp.x_rows = a->x_rows;
+  pp.R = a->R;
+  pp.K = a->K;
+  pp.n_experts = a->n_experts;
+  pp.tile_rows = L.tile_rows;
+  pp.quantise = !rows8;
+  pp.q = reinterpret_cast<int8_t*>(ws + L.q);
+  pp.a = reinterpret_cast<float*>(ws + L.a);
+  pp.sched = reinterpret_cast<i8::Sched*>(ws + L.sched);
+  pp.counters = reinterpret_cast<int32_t*>(ws + L.counters);
+  pp.status = reinterpret_cast<uint32_t*>(ws + L.status);
+  if ((a->x_dtype == MOE_F32 ? i8::launch_prepare<false>(pp, s) : i8::launch_prepare<true>(pp, s)) != cudaSuccess)
+    return MOE_ERR_CUDA;
+
+  i8::Params p{};
+  p.sched = pp.sched;
+  p.a = rows8 ? a->x_scale : pp.a;
+  p.gate = a->gate;
+  p.s0 = static_cast<const __nv_bfloat16*>(a->s);
+  p.s1 = static_cast<const __nv_bfloat16*>(a->s_up);
+  p.out = a->out;
+  p.counters = pp.counters;
+  p.part = reinterpret_cast<int32_t*>(ws + L.part);
+  p.status = pp.status;
+  p.R = a->R;
+  p.N = static_cast<int32_t>(a->N);
+  p.n_experts = a->n_experts;
+  p.kb = static_cast<int32_t>((a->K + i8::BK - 1) / i8::BK);
+  p.act = a->activation;
+  const void* q = rows8 ? a->x : static_cast<const void*>(pp.q);
+  const bool ob = a->out_dtype == MOE_BF16;
+  auto form = [&](auto rows) {
+    constexpr int ROWS = decltype(rows)::value;
+    if (dual) return ob ? i8::launch_stream<ROWS, true, true>(a, q, p, s) : i8::launch_stream<ROWS, true, false>(a, q, p, s);
+    return ob ? i8::launch_stream<ROWS, false, true>(a, q, p, s) : i8::launch_stream<ROWS, false, false>(a, q, p, s);
+  };
+  const cudaError_t e = L.tile_rows == 64 ? form(std::integral_constant<int, 64>{})
+                                          : form(std::integral_constant<int, 128>{});
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"
