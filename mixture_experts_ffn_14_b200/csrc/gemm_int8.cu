@@ -246,6 +246,7 @@ struct Params {
   uint32_t* status;
   int64_t R;
   int32_t N, n_experts, nt, kb, act;
+  int32_t group_rows, group_limit;  // pair form: row tiles per L2 group (tile_order.cuh)
 };
 
 // Gate activation in fp32: z * sigmoid(.) forms, which keep the relative accuracy
@@ -274,9 +275,9 @@ __device__ __forceinline__ int expert_of(const int32_t* pre, int n, int m) {
 // ---- stream form ----------------------------------------------------------
 // For few rows per expert: the weights' columns are the MMA's M side and the tile's
 // tokens (at most ROWS) its N side, so the tensor work follows the tokens there are
-// and the kernel is bound by reading each weight byte once. All CTAs take equal runs
-// of the (tile, K block) sequence; a tile that the runs cut is summed from its parts:
-// every CTA but the one that brings the last part stores its 32-bit sums and counts
+// and the kernel is bound by reading each weight byte once. The tiles that do not fill
+// a wave are cut into equal runs of K blocks; a tile that the runs cut is summed from its
+// parts: every CTA but the one that brings the last part stores its 32-bit sums and counts
 // its K blocks, that one adds all parts (integers: any order gives the same sum) and
 // finishes the tile. No CTA waits for another.
 
@@ -291,11 +292,11 @@ struct StreamCfg {
   static constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 256;  // alignment slack, barriers; + schedule
 };
 constexpr int XBOX_ROWS = 32;
-constexpr int kMinRun = 2;
+constexpr int kMinRun = 8;  // K blocks of a run at least: 1024 of K
 
 struct Seg {
   int e, row0, rows, n0, kb0, kb1;
-  int64_t tile0;  // first K block of the tile in the whole sequence
+  int64_t tile0;  // cut part: first K block of the tile in its sequence
 };
 
 template <int ROWS, bool DUAL, bool OB>
@@ -341,30 +342,47 @@ __global__ void __launch_bounds__(256, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int64_t total = static_cast<int64_t>(pre[p.n_experts]) * p.nt * p.kb;
-  // Runs of at least kMinRun K blocks: no run is empty, and the last CTAs of a small
-  // problem have nothing to do.
+  // Tiles: waves of one whole tile per CTA, whose neighbours in the order (next columns of
+  // the same weights) run side by side, and a remainder of fewer tiles than CTAs, cut into
+  // equal runs of K blocks. The cut part goes first, so that joining its sums hides
+  // behind the whole tiles.
+  const int64_t tiles = static_cast<int64_t>(pre[p.n_experts]) * p.nt;
+  const int64_t waves = tiles / gridDim.x, whole0 = tiles - waves * gridDim.x;
+  const int64_t total = whole0 * p.kb;  // K blocks of the cut part
+  // Runs of at least kMinRun K blocks: no run is empty, the last CTAs may have none.
   const int64_t G = min(static_cast<int64_t>(gridDim.x), max(total / kMinRun, int64_t(1)));
   const int64_t me = blockIdx.x;
   const int64_t lo = me < G ? total * me / G : total, hi = me < G ? total * (me + 1) / G : total;
 
-  // The part of this CTA's run that starts at `pos`: one tile or a piece of it.
-  // Row tiles run fastest within an expert, so tiles that share weights follow
-  // one another.
-  auto segment = [&](int64_t pos, Seg& s) {
-    const int64_t tile = pos / p.kb;
-    s.tile0 = tile * p.kb;
-    s.kb0 = static_cast<int>(pos - s.tile0);
-    const int64_t end = hi - s.tile0;
-    s.kb1 = static_cast<int>(end < p.kb ? end : p.kb);
+  struct Cursor {
+    int64_t pos, wave;
+  };
+  auto next = [&](Cursor& c, Seg& s) -> bool {
+    int64_t tile;
+    if (c.pos < hi) {
+      tile = c.pos / p.kb;
+      s.tile0 = tile * p.kb;
+      s.kb0 = static_cast<int>(c.pos - s.tile0);
+      s.kb1 = static_cast<int>(min(hi - s.tile0, static_cast<int64_t>(p.kb)));
+      c.pos = s.tile0 + s.kb1;
+    } else if (c.wave < waves) {
+      tile = whole0 + c.wave * gridDim.x + me;
+      s.tile0 = 0;
+      s.kb0 = 0;
+      s.kb1 = p.kb;
+      ++c.wave;
+    } else {
+      return false;
+    }
     s.e = expert_of(pre, p.n_experts, static_cast<int>(tile / p.nt));
     const int mt = pre[s.e + 1] - pre[s.e];
     const int local = static_cast<int>(tile - static_cast<int64_t>(pre[s.e]) * p.nt);
-    const int m = local % mt;
+    const int m = local % mt;  // row tiles run fastest: those that share weights follow one another
     s.n0 = (local / mt) * (DUAL ? 128 : 256);
     const int cnt = p.sched->cnt[s.e];
     s.row0 = p.sched->off[s.e] + m * ROWS;
     s.rows = min(ROWS, cnt - m * ROWS);
+    return true;
   };
 
   if (warp == 0 && lane == 0) {
@@ -374,8 +392,8 @@ __global__ void __launch_bounds__(256, 1)
     uint32_t phase = 0;
     bool ok = true;
     Seg s;
-    for (int64_t pos = lo; ok && pos < hi; pos = s.tile0 + s.kb1) {
-      segment(pos, s);
+    Cursor cur{lo, 0};
+    while (ok && next(cur, s)) {
       const int boxes = (s.rows + XBOX_ROWS - 1) / XBOX_ROWS;
       for (int kb = s.kb0; kb < s.kb1; ++kb) {
         if (!mbar_wait(&empty_bar[stage], phase ^ 1, kWaitLimitNs) || *abort_flag) {
@@ -414,8 +432,8 @@ __global__ void __launch_bounds__(256, 1)
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
     Seg s;
-    for (int64_t pos = lo; ok && pos < hi; pos = s.tile0 + s.kb1) {
-      segment(pos, s);
+    Cursor cur{lo, 0};
+    while (ok && next(cur, s)) {
       if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1, kWaitLimitNs) || *abort_flag) ok = false;
       tc_fence_after();
       const uint32_t d = tmem_base + acc * C::ACC_COLS;
@@ -464,8 +482,8 @@ __global__ void __launch_bounds__(256, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     Seg s;
-    for (int64_t pos = lo; pos < hi; pos = s.tile0 + s.kb1) {
-      segment(pos, s);
+    Cursor cur{lo, 0};
+    while (next(cur, s)) {
       if (!warp_wait(&tfull_bar[acc], acc_phase, abort_flag)) {
         atomicOr(p.status, kStatusEpilogueTimeout);
         *abort_flag = 1;
@@ -563,11 +581,336 @@ __global__ void __launch_bounds__(256, 1)
   }
 }
 
+// ---- pair form --------------------------------------------------------------
+// For many rows per expert: a cluster of two CTAs on an SM pair computes 256 rows x 256
+// accumulator columns with cta_group::2 (128 gate and 128 up columns of a gated pair).
+// Each CTA loads its own 128 rows and 128 weight columns, 32 KB a stage for 512 tensor
+// cycles, and keeps its 128 rows of the sums in its own TMEM (two accumulators, so the
+// epilogue of one tile runs beside the next one's products). Tiles are handed out in
+// order from a counter, row tiles of one weight tile next to one another, so that the
+// pairs that run together share weights in L2 (tile_order.cuh).
+
+constexpr int PAIR_ROWS = 256;
+constexpr int PX_BYTES = 128 * BK;              // 16 KB: this CTA's 128 rows
+constexpr int PSTAGE_BYTES = PX_BYTES + WBOX;   // 32 KB
+constexpr int PSTAGES = 6;
+constexpr int PQ = 4;             // tile-id queue: the producer leads by at most 3 tiles
+constexpr int PQ_READERS = 10;    // odd producer, MMA thread, 4 epilogue warps x 2 CTAs
+constexpr int PSMEM = PSTAGES * PSTAGE_BYTES + 1024 + 256 + (kMaxExperts + 1) * 4;
+static_assert(PSMEM <= 232448, "shared memory above the per-block limit");
+static_assert((2 * PSTAGES + 4 + 2 * PQ + 1) * 8 + 8 + 4 * PQ <= 256, "barrier area too small");
+
+// Bounded wait with cluster-scope acquire (for barriers that the other CTA arrives on).
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+  auto once = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (once()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (once()) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+
+// One row (thread) of an epilogue warp: 16-column steps of the accumulator, scaled,
+// activated and stored as 32 or 64 contiguous bytes.
+template <bool DUAL, bool OB>
+__device__ __forceinline__ void pair_epilogue(const Params& p, int e, int n0, uint32_t tb, int64_t row, bool valid) {
+  const int64_t se = static_cast<int64_t>(e) * p.N;
+  const float a = valid ? __ldg(p.a + row) : 0.0f;
+  const float g = valid && p.gate != nullptr ? __ldg(p.gate + row) : 1.0f;
+  auto scales = [&](const __nv_bfloat16* s, int c, float (&f)[16]) {
+    const uint4* q = reinterpret_cast<const uint4*>(s + se + c);
+    const uint4 u = __ldg(q), v = __ldg(q + 1);
+    const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[2 * j] = bf16_lo(w[j]);
+      f[2 * j + 1] = bf16_hi(w[j]);
+    }
+  };
+  auto put16 = [&](int c, const float (&y)[16]) {
+    if (!valid) return;
+    if (OB) {
+      uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * p.N + c);
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+        d[v] = make_uint4(pack_bf16x2(y[8 * v], y[8 * v + 1]), pack_bf16x2(y[8 * v + 2], y[8 * v + 3]),
+                          pack_bf16x2(y[8 * v + 4], y[8 * v + 5]), pack_bf16x2(y[8 * v + 6], y[8 * v + 7]));
+    } else {
+      float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.N + c);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) d[v] = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
+    }
+  };
+#pragma unroll 1
+  for (int c = 0; c < (DUAL ? 128 : 256); c += DUAL ? 16 : 32) {
+    if (n0 + c >= p.N) break;  // N is a multiple of 16
+    const bool second = DUAL || n0 + c + 16 < p.N;
+    float s0[16], s1[16], y[16];
+    scales(p.s0, n0 + c, s0);
+    if (second) scales(DUAL ? p.s1 : p.s0, DUAL ? n0 + c : n0 + c + 16, s1);
+    uint32_t u[16], v[16];
+    tmem_ld16x2(tb + c, tb + c + (DUAL ? 128 : 16), u, v);
+    if (DUAL) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float z = static_cast<float>(static_cast<int>(u[j])) * a * s0[j];
+        const float z1 = static_cast<float>(static_cast<int>(v[j])) * a * s1[j];
+        y[j] = act_f32(z, p.act) * z1 * g;
+      }
+      put16(n0 + c, y);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[j] = static_cast<float>(static_cast<int>(u[j])) * a * s0[j] * g;
+      put16(n0 + c, y);
+      if (second) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] = static_cast<float>(static_cast<int>(v[j])) * a * s1[j] * g;
+        put16(n0 + c + 16, y);
+      }
+    }
+  }
+}
+
+template <bool DUAL, bool OB>
+__global__ void __launch_bounds__(256, 1)
+    moe_int8_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
+                         const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + PSTAGES * PSTAGE_BYTES);
+  uint64_t* empty_bar = full_bar + PSTAGES;
+  uint64_t* tfull_bar = empty_bar + PSTAGES;
+  uint64_t* tempty_bar = tfull_bar + 2;
+  uint64_t* qfull_bar = tempty_bar + 2;
+  uint64_t* qempty_bar = qfull_bar + PQ;
+  uint64_t* drain_bar = qempty_bar + PQ;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* tile_q = abort_flag + 1;
+  int32_t* pre = reinterpret_cast<int32_t*>(full_bar) + 64;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();  // 0: issues the MMAs of the pair
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < PSTAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull_bar[b], 1);
+      mbar_init(&tempty_bar[b], 2 * 4);
+    }
+    for (int i = 0; i < PQ; ++i) {
+      mbar_init(&qfull_bar[i], 1);
+      mbar_init(&qempty_bar[i], PQ_READERS);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_w0);
+    if (DUAL) tma_prefetch_desc(&tm_w1);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  for (int e = threadIdx.x; e <= p.n_experts; e += 256) pre[e] = p.sched->pre[e];
+  tc_fence_before();
+  cluster_sync();  // barriers of both CTAs initialised, TMEM allocated in both
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int ntiles = pre[p.n_experts] * p.nt;
+
+  struct Tile {
+    int e, row0, rows, n0;
+  };
+  auto decode = [&](int tile) {
+    Tile t;
+    t.e = expert_of(pre, p.n_experts, tile / p.nt);
+    const int mt = pre[t.e + 1] - pre[t.e];
+    int m, c, ks;
+    tile_coords(tile - pre[t.e] * p.nt, mt, p.nt, group_for(mt, p.group_rows, p.group_limit), m, c, ks);
+    t.row0 = p.sched->off[t.e] + m * PAIR_ROWS;
+    t.rows = min(PAIR_ROWS, p.sched->cnt[t.e] - m * PAIR_ROWS);
+    t.n0 = c * (DUAL ? 128 : 256);
+    return t;
+  };
+  // Queue operations: the tile id, -1 when none is left, -2 when a wait ran out.
+  auto q_fill = [&](int i) -> int {  // even CTA's producer
+    const int slot = i % PQ;
+    const uint32_t ph = (i / PQ) & 1;
+    if (!mbar_wait_cluster(&qempty_bar[slot], ph ^ 1) || *abort_flag) return -2;
+    const int t = atomicAdd(p.counters, 1);
+    const int tile = t < ntiles ? t : -1;
+    tile_q[slot] = tile;
+    st_shared_cluster_u32(mapa_shared(const_cast<int*>(&tile_q[slot]), 1), static_cast<uint32_t>(tile));
+    mbar_arrive(&qfull_bar[slot]);
+    mbar_arrive_cluster(mapa_shared(&qfull_bar[slot], 1));
+    return tile;
+  };
+  auto q_take = [&](int i) -> int {  // one thread of any other role
+    const int slot = i % PQ;
+    const uint32_t ph = (i / PQ) & 1;
+    if (!mbar_wait_cluster(&qfull_bar[slot], ph) || *abort_flag) return -2;
+    const int tile = tile_q[slot];
+    mbar_arrive_cluster(mapa_shared(&qempty_bar[slot], 0));
+    return tile;
+  };
+  auto q_take_warp = [&](int i) -> int {  // a whole epilogue warp, one arrive
+    const int slot = i % PQ;
+    const uint32_t ph = (i / PQ) & 1;
+    const bool ok = mbar_wait_cluster(&qfull_bar[slot], ph) && !*abort_flag;
+    if (!__all_sync(0xffffffffu, ok)) return -2;
+    const int tile = tile_q[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(mapa_shared(&qempty_bar[slot], 0));
+    return tile;
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ producer --
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const int tile = rank == 0 ? q_fill(i) : q_take(i);
+      if (tile == -2) ok = false;
+      if (tile < 0) break;
+      const Tile t = decode(tile);
+      const int row = t.row0 + 128 * static_cast<int>(rank);
+      // gated pair: the even CTA holds the gate columns, the odd one the up columns
+      const CUtensorMap* wmap = DUAL && rank == 1 ? &tm_w1 : &tm_w0;
+      const int n = DUAL ? t.n0 : t.n0 + 128 * static_cast<int>(rank);
+      for (int kb = 0; kb < p.kb; ++kb) {
+        if (!mbar_wait(&empty_bar[stage], phase ^ 1, kWaitLimitNs) || *abort_flag) {
+          ok = false;
+          break;
+        }
+        uint8_t* xs = smem + stage * PSTAGE_BYTES;
+        const uint32_t bar0 = mapa_shared(&full_bar[stage], 0);
+        if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * PSTAGE_BYTES);
+        tma_load_2d_pair(xs, &tm_x, bar0, kb * BK, row);
+        tma_load_3d_pair(xs + PX_BYTES, wmap, bar0, n, kb * BK, t.e);
+        if (++stage == PSTAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok) {
+      atomicOr(p.status, kStatusProducerTimeout);
+      *abort_flag = 1;
+    }
+    // Every stage's last release (an arrive of the pair's MMA commit) has landed
+    // before this CTA may leave; after a timeout this wait is bounded as well.
+    for (int i = 0; i < PSTAGES; ++i) {
+      if (!mbar_wait(&empty_bar[stage], phase ^ 1, kWaitLimitNs)) {
+        atomicOr(p.status, kStatusProducerTimeout);
+        break;
+      }
+      if (++stage == PSTAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ----------------------------------------------------------------- MMA --
+    constexpr uint32_t idesc = idesc_s8_s32(PAIR_ROWS, 256, 0, 1);
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const int tile = q_take(i);
+      if (tile == -2) ok = false;
+      if (tile < 0) break;
+      if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1) || *abort_flag) ok = false;
+      tc_fence_after();
+      const uint32_t d = tmem_base + acc * 256;
+      for (int kb = 0; ok && kb < p.kb; ++kb) {
+        if (!mbar_wait(&full_bar[stage], phase, kWaitLimitNs) || *abort_flag) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t xs = smem_u32(smem + stage * PSTAGE_BYTES), ws = xs + PX_BYTES;
+#pragma unroll
+        for (int k = 0; k < BK / 32; ++k)
+          umma_s8_pair(d, smem_desc_sw128(xs + k * 32, 16, 1024), smem_desc_sw128(ws + k * 4096, WBOX, 1024), idesc,
+                       kb > 0 || k > 0);
+        umma_commit_pair(&empty_bar[stage], 0x3);
+        if (++stage == PSTAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (ok) umma_commit_pair(&tfull_bar[acc], 0x3);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+    if (!ok) {
+      atomicOr(p.status, kStatusMmaTimeout);
+      *abort_flag = 1;
+      umma_commit_pair(drain_bar, 0x1);  // unwinding: the tensor cores are done before TMEM is freed
+      mbar_wait(drain_bar, 0, kWaitLimitNs);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue --
+    const int q = warp - 4;
+    const uint32_t tempty0[2] = {mapa_shared(&tempty_bar[0], 0), mapa_shared(&tempty_bar[1], 0)};
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int i = 0;; ++i) {
+      const int tile = q_take_warp(i);
+      if (tile == -1) break;
+      if (tile == -2 || !warp_wait(&tfull_bar[acc], acc_phase, abort_flag)) {
+        atomicOr(p.status, kStatusEpilogueTimeout);
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const Tile t = decode(tile);
+      const int r = 128 * static_cast<int>(rank) + 32 * q + lane;
+      pair_epilogue<DUAL, OB>(p, t.e, t.n0, tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * 256,
+                              static_cast<int64_t>(t.row0) + r, r < t.rows);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty0[acc]);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while its peer may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
 // ------------------------------------------------------------------- host --
 
 struct Layout {
   size_t status, sched, counters, q, a, part, total;
-  int32_t tile_rows;  // rows of a tile: 64 or 128 (stream form)
+  int32_t tile_rows;  // rows of a tile: 64 or 128 (stream form), 256 (pair form)
 };
 
 Layout plan(int64_t R, int64_t K, int32_t n_experts, moe_dtype_t x_dtype) {
@@ -578,7 +921,7 @@ Layout plan(int64_t R, int64_t K, int32_t n_experts, moe_dtype_t x_dtype) {
     o = (o + bytes + 255) / 256 * 256;
     return at;
   };
-  L.tile_rows = R <= 48 * static_cast<int64_t>(n_experts) ? 64 : 128;
+  L.tile_rows = R <= 48 * static_cast<int64_t>(n_experts) ? 64 : (R <= 96 * static_cast<int64_t>(n_experts) ? 128 : 256);
   L.status = take(256);
   L.sched = take(sizeof(Sched));
   L.counters = take(sizeof(int32_t) * kMaxCtas);
@@ -586,7 +929,8 @@ Layout plan(int64_t R, int64_t K, int32_t n_experts, moe_dtype_t x_dtype) {
     L.q = take(static_cast<size_t>(R) * K);
     L.a = take(sizeof(float) * R);
   }
-  L.part = take(sizeof(int32_t) * 2 * kMaxCtas * 256 * static_cast<size_t>(L.tile_rows));
+  L.part = o;
+  if (L.tile_rows < PAIR_ROWS) take(sizeof(int32_t) * 2 * kMaxCtas * 256 * static_cast<size_t>(L.tile_rows));
   L.total = o;
   return L;
 }
@@ -634,6 +978,51 @@ cudaError_t launch_stream(const moe_int8_args_t* a, const void* q, Params p, cud
   const int grid = static_cast<int>(std::min<int64_t>(std::min(device_sm_count(), kMaxCtas), most));
   kern<<<grid, 256, kSmem, s>>>(tx, tw0, tw1, p);
   return cudaGetLastError();
+}
+
+template <bool DUAL, bool OB>
+cudaError_t launch_pair(const moe_int8_args_t* a, const void* q, Params p, cudaStream_t s) {
+  auto kern = moe_int8_pair_kernel<DUAL, OB>;
+  const cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), PSMEM);
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = PSMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // Clusters of two that fit at once on this device (queried once per device).
+  const int max_pairs = once_per_device(reinterpret_cast<const void*>(&launch_pair<DUAL, OB>), [](const void*) {
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(2 * (device_sm_count() / 2), 1, 1);
+    c.blockDim = dim3(256, 1, 1);
+    c.dynamicSmemBytes = PSMEM;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, moe_int8_pair_kernel<DUAL, OB>, &c) != cudaSuccess || n <= 0)
+      n = device_sm_count() / 2;
+    return n;
+  });
+  CUtensorMap tx, tw0, tw1;
+  if (!row_map(&tx, q, a, 128) || !weight_map(&tw0, a->w, a) || !weight_map(&tw1, DUAL ? a->w_up : a->w, a))
+    return cudaErrorInvalidValue;
+  p.nt = static_cast<int32_t>((a->N + (DUAL ? 127 : 255)) / (DUAL ? 128 : 256));
+  p.group_rows = row_group_size(PAIR_ROWS, (a->K + 1) / 2, tc::kL2GroupBytes);
+  p.group_limit = row_group_size(PAIR_ROWS, (a->K + 1) / 2, tc::kL2UngroupedBytes);
+  const int64_t most = ((a->R + PAIR_ROWS - 1) / PAIR_ROWS + a->n_experts) * p.nt;
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(most, max_pairs)), 1, 1);
+  return cudaLaunchKernelEx(&cfg, kern, tx, tw0, tw1, p);
 }
 
 template <bool BF16>
@@ -721,8 +1110,11 @@ moe_status_t moe_int8_product(const moe_int8_args_t* a, void* workspace, size_t 
     if (dual) return ob ? i8::launch_stream<ROWS, true, true>(a, q, p, s) : i8::launch_stream<ROWS, true, false>(a, q, p, s);
     return ob ? i8::launch_stream<ROWS, false, true>(a, q, p, s) : i8::launch_stream<ROWS, false, false>(a, q, p, s);
   };
-  const cudaError_t e = L.tile_rows == 64 ? form(std::integral_constant<int, 64>{})
-                                          : form(std::integral_constant<int, 128>{});
+  cudaError_t e;
+  if (L.tile_rows == 64) e = form(std::integral_constant<int, 64>{});
+  else if (L.tile_rows == 128) e = form(std::integral_constant<int, 128>{});
+  else if (dual) e = ob ? i8::launch_pair<true, true>(a, q, p, s) : i8::launch_pair<true, false>(a, q, p, s);
+  else e = ob ? i8::launch_pair<false, true>(a, q, p, s) : i8::launch_pair<false, false>(a, q, p, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
