@@ -44,6 +44,29 @@ struct Sched {
 
 // ---------------------------------------------------------------- prepare --
 
+// Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) into this
+// CTA's shared memory, its bytes counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Named barrier of n threads that tells whether `v` held for all of them.
+__device__ __forceinline__ bool barrier_and(int id, int n, bool v) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(n)
+      : "memory");
+  return all != 0;
+}
+
 struct PrepParams {
   const void* x;
   const int32_t* index;
@@ -58,7 +81,7 @@ struct PrepParams {
   uint32_t* status;
 };
 
-constexpr int kPrepThreads = 256;
+constexpr int kPrepThreads = 256;   // of the schedule
 
 // Prefix sums of the experts' rows and row tiles by one CTA. Counts that are
 // negative or run past R are cut off (status bit kStatusBounds), so that no row
@@ -67,6 +90,8 @@ __device__ void make_schedule(const PrepParams& p) {
   constexpr int PER = kMaxExperts / kPrepThreads;
   __shared__ long long part_rows[kPrepThreads / 32];
   __shared__ int part_tiles[kPrepThreads / 32];
+  __shared__ int any_bad;
+  auto sync = [] { asm volatile("bar.sync 15, %0;" ::"n"(kPrepThreads) : "memory"); };  // part of the CTA
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   for (int i = tid; i < kMaxCtas; i += kPrepThreads) p.counters[i] = 0;
   long long c[PER], rows = 0;
@@ -89,7 +114,7 @@ __device__ void make_schedule(const PrepParams& p) {
     if (lane >= o) inc += v;
   }
   if (lane == 31) part_rows[warp] = inc;
-  __syncthreads();
+  sync();
   long long at = inc - rows;
   for (int w = 0; w < warp; ++w) at += part_rows[w];
   int tiles = 0, mine[PER];
@@ -114,7 +139,7 @@ __device__ void make_schedule(const PrepParams& p) {
     if (lane >= o) tinc += v;
   }
   if (lane == 31) part_tiles[warp] = tinc;
-  __syncthreads();
+  sync();
   int t = tinc - tiles;
   for (int w = 0; w < warp; ++w) t += part_tiles[w];
 #pragma unroll
@@ -124,112 +149,261 @@ __device__ void make_schedule(const PrepParams& p) {
     t += mine[j];
     if (e == p.n_experts - 1) p.sched->pre[p.n_experts] = t;
   }
-  const int any = __syncthreads_or(bad);
-  if (tid == 0) *p.status = any ? kStatusBounds : 0u;
+  if (tid == 0) any_bad = 0;
+  sync();
+  if (bad) any_bad = 1;
+  sync();
+  if (tid == 0) *p.status = any_bad ? kStatusBounds : 0u;
+}
+
+// Eight values of a row as they lie in memory: 16 bytes (bf16) or 32.
+template <bool BF16>
+struct Raw {
+  uint4 v[BF16 ? 1 : 2];
+};
+
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load_raw(const void* row, int v) {
+  Raw<BF16> r;
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) r.v[i] = static_cast<const uint4*>(row)[v * (BF16 ? 1 : 2) + i];
+  return r;
 }
 
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* row, int64_t v, float (&f)[8]) {
-  if (BF16) {
-    const uint4 u = static_cast<const uint4*>(row)[v];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void unpack(const Raw<BF16>& r, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+    const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(w[j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      if (BF16) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      } else {
+        f[4 * i + j] = __uint_as_float(w[j]);
+      }
     }
-  } else {
-    const float4 a = static_cast<const float4*>(row)[2 * v], b = static_cast<const float4*>(row)[2 * v + 1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
 }
 
-// x / (top / 127) rounded to nearest, ties to even, as the exact quotient rounds.
-// The fp32 quotient is off by at most 127 * 2 * 2^-24 < 2e-5; one further than 1e-4
-// from a half rounds as the exact one does, the others (and those whose reciprocal
-// left the fp32 range) are divided in 64 bits, where 127 x is exact and no quotient
-// of two fp32 numbers is nearer to a half than 2^-33 without being one.
-__device__ __forceinline__ int quantise(float x, float r, float top) {
-  const float y = x * r;
-  float q = rintf(y);
-  if (!(fabsf(fabsf(y - q) - 0.5f) >= 1e-4f)) q = static_cast<float>(rint(127.0 * x / top));
-  return static_cast<int>(q);
+// A quotient this close to a half (of the fp32 product x * (127 / top), which is off by
+// at most 127 * 2^-24 < 8e-6, the reciprocal's rounding) is decided exactly.
+constexpr float kNearHalf = 0.5f - 1e-5f;
+
+// 127 x / top rounded to nearest, ties to even, as the exact quotient rounds; `low` is
+// the integer below it. Compares 254 x with (2 low + 1) top: both products in two
+// parts (value and exact remainder; 32 bits each, so the parts' differences are exact).
+__device__ __forceinline__ int quantise_near_half(float x, float top, float low) {
+  const float odd = 2.0f * low + 1.0f;
+  const float a = 254.0f * x, b = odd * top;
+  const float d = (a - b) + (fmaf(254.0f, x, -a) - fmaf(odd, top, -b));
+  const int l = static_cast<int>(low);
+  return d > 0.0f ? l + 1 : (d < 0.0f ? l : l + (l & 1));
 }
 
-// One row per CTA: its largest magnitude (as bits, so that NaN and infinity win), then
-// the quotients. Rows of up to kPrepThreads * 8 * MAXV values stay in registers
-// between the two passes; longer ones (MAXV = 0) are read again, from L2.
-template <bool BF16, int MAXV>
-__global__ void __launch_bounds__(kPrepThreads) moe_int8_prepare_kernel(const __grid_constant__ PrepParams p) {
+// The vectors that hold such a quotient, and those of rows next to the ends of the fp32
+// range (scale != 1).
+template <bool BF16>
+__device__ __noinline__ uint2 quantise8_near(Raw<BF16> r, float rcp, float scale, float top) {
+  float f[8];
+  unpack<BF16>(r, f);
+  uint32_t q[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = f[j] * scale, y = x * rcp, m = rintf(y);
+    int n = static_cast<int>(m);
+    if (fabsf(y - m) > kNearHalf) n = quantise_near_half(x, top, y < m ? m - 1.0f : m);
+    q[j / 4] |= static_cast<uint32_t>(n & 0xff) << (8 * (j % 4));
+  }
+  return make_uint2(q[0], q[1]);
+}
+
+// What the quotients of a row need, from the bits of its largest magnitude.
+struct RowScale {
+  float rcp, scale, top;
+  bool zero;  // q = 0; a = NaN or 0
+  bool far;   // next to an end of the fp32 range: every vector takes the careful path
+
+  __device__ __forceinline__ explicit RowScale(uint32_t top_bits) {
+    const float t = __uint_as_float(top_bits);
+    zero = top_bits >= 0x7f800000u || top_bits == 0;
+    // Such rows are moved by a power of two (exact for every value that is not far
+    // below the largest), so that no product leaves the range.
+    scale = t < 1e-30f ? 0x1p80f : (t > 1e30f ? 0x1p-30f : 1.0f);
+    far = scale != 1.0f;
+    top = t * scale;
+    rcp = 127.0f / top;
+  }
+};
+
+__device__ __forceinline__ float row_step(uint32_t top_bits) {
+  return top_bits < 0x7f800000u ? __uint_as_float(top_bits) / 127.0f : __uint_as_float(0x7fc00000u);
+}
+
+// Eight quotients to bytes. Adding 1.5 * 2^23 to a product leaves it rounded to an
+// integer (ties to even) in the low mantissa bits; a vector with a quotient next to a
+// half (one in six thousand) is looked at again. A warp that does holds up its row's
+// group at the next barrier, so these must be few.
+template <bool BF16>
+__device__ __forceinline__ uint2 quantise8(Raw<BF16> r, const RowScale& s) {
+  if (s.zero) return make_uint2(0, 0);
+  constexpr float kMagic = 12582912.0f;
+  float f[8];
+  unpack<BF16>(r, f);
+  uint32_t t[8];
+  float off = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float m = fmaf(f[j], s.rcp, kMagic);
+    t[j] = __float_as_uint(m);
+    off = fmaxf(off, fabsf(fmaf(f[j], s.rcp, kMagic - m)));
+  }
+  if (off > kNearHalf || s.far) return quantise8_near<BF16>(r, s.rcp, s.scale, s.top);
+  return make_uint2(
+      __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
+      __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
+}
+
+// Largest magnitude of eight values, as fp32 bits (bf16: two 16-bit maxima at a time).
+template <bool BF16>
+__device__ __forceinline__ void largest(const Raw<BF16>& x, uint32_t& top) {
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+    const uint32_t w[4] = {x.v[i].x, x.v[i].y, x.v[i].z, x.v[i].w};
+    if (BF16) {
+      const uint32_t m = __vimax3_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu, w[2] & 0x7fff7fffu);
+      top = __vimax3_u16x2(m, w[3] & 0x7fff7fffu, top);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, w[j] & 0x7fffffffu);
+    }
+  }
+}
+
+// fp32 bits of what largest() gathered.
+template <bool BF16>
+__device__ __forceinline__ uint32_t largest_bits(uint32_t top) {
+  return BF16 ? max(top << 16, top & 0xffff0000u) : top;
+}
+
+// Rows to 8 bits, bound by memory: groups of NT threads take rows in turn; up to kRing
+// rows of each group are on their way into shared memory as bulk copies while one is worked
+// on, and a row goes from there to registers once (its largest magnitude as bits, so
+// that NaN and infinity win; then the quotients). One barrier per row. The schedule is
+// made by the last CTA, which has the fewest rows.
+constexpr int kPrepCta = 1024;
+constexpr int kRing = 4;
+constexpr int kRingBytes = 200 * 1024;  // shared memory for rows on their way
+constexpr int kPrepVec = 4;             // vectors of 8 values per thread
+
+template <bool BF16, int NT>
+__global__ void __launch_bounds__(kPrepCta, 1)
+    moe_int8_prepare_kernel(const __grid_constant__ PrepParams p, int32_t ring) {
+  constexpr int GROUPS = kPrepCta / NT, WARPS = NT / 32;
+  extern __shared__ __align__(128) uint8_t rows_smem[];
+  __shared__ __align__(8) uint64_t full[GROUPS][kRing];
+  __shared__ int real_row[GROUPS][kRing];
+  __shared__ uint32_t part[GROUPS][2][WARPS < 32 ? 32 : WARPS];
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x < kPrepThreads) make_schedule(p);
+  if (!p.quantise) return;
+  const int group = threadIdx.x / NT, tid = threadIdx.x % NT, lane = threadIdx.x % 32, warp = tid / 32;
+  const int64_t row_bytes = p.K * (BF16 ? 2 : 4);
+  const int nvec = static_cast<int>(p.K / 8);
+  uint8_t* mine = rows_smem + group * ring * row_bytes;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * GROUPS;
+  const int64_t r0 = blockIdx.x + static_cast<int64_t>(group) * gridDim.x;
+  auto fetch = [&](int64_t r, int slot) {  // thread 0 of the group
+    const int64_t src = p.index != nullptr ? p.index[r] : r;
+    const bool real = src >= 0 && src < p.x_rows;
+    real_row[group][slot] = real;
+    if (real) {
+      mbar_arrive_expect_tx(&full[group][slot], static_cast<uint32_t>(row_bytes));
+      bulk_load(mine + slot * row_bytes, static_cast<const uint8_t*>(p.x) + src * row_bytes,
+                static_cast<uint32_t>(row_bytes), &full[group][slot]);
+    } else {
+      mbar_arrive(&full[group][slot]);
+    }
+  };
+  if (tid == 0) {
+    for (int s = 0; s < ring; ++s) mbar_init(&full[group][s], 1);
+    fence_mbar_init();
+    for (int s = 0; s < ring; ++s)
+      if (r0 + s * step < p.R) fetch(r0 + s * step, s);
+  }
+  __syncthreads();
+  int slot = 0;
+  uint32_t phase = 0, flip = 0;
+  for (int64_t r = r0; r < p.R; r += step) {
+    bool ok = mbar_wait(&full[group][slot], phase, kWaitLimitNs);
+    const bool real = ok && real_row[group][slot];
+    const uint8_t* row = mine + slot * row_bytes;
+    Raw<BF16> raw[kPrepVec];
+    uint32_t top_bits = 0;
+    if (real) {
+#pragma unroll
+      for (int i = 0; i < kPrepVec; ++i)
+        if (tid + i * NT < nvec) raw[i] = load_raw<BF16>(row, tid + i * NT);
+#pragma unroll
+      for (int i = 0; i < kPrepVec; ++i)
+        if (tid + i * NT < nvec) largest<BF16>(raw[i], top_bits);
+    }
+    top_bits = __reduce_max_sync(0xffffffffu, largest_bits<BF16>(top_bits));
+    if (NT == 32) {
+      ok = __all_sync(0xffffffffu, ok);
+      __syncwarp();
+    } else {
+      if (lane == 0) part[group][flip][warp] = top_bits;
+      ok = barrier_and(1 + group, NT, ok);  // all or none of the group go on
+      top_bits = __reduce_max_sync(0xffffffffu, lane < WARPS ? part[group][flip][lane] : 0u);
+    }
+    if (!ok) {
+      if (tid == 0) atomicOr(p.status, kStatusProducerTimeout);
+      return;
+    }
+    // the row is in registers: its slot takes the next one
+    if (tid == 0 && r + ring * step < p.R) fetch(r + ring * step, slot);
+    const RowScale rs(top_bits);
+    if (tid == 0) p.a[r] = row_step(top_bits);
+    uint2* dst = reinterpret_cast<uint2*>(p.q + r * p.K);
+#pragma unroll
+    for (int i = 0; i < kPrepVec; ++i)
+      if (tid + i * NT < nvec)
+        dst[tid + i * NT] = quantise8<BF16>(raw[i], rs);
+    flip ^= 1;
+    if (++slot == ring) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+}
+
+// Rows too long for two of them to be in shared memory: one row per CTA, read twice
+// (the second time from L2).
+template <bool BF16>
+__global__ void __launch_bounds__(kPrepCta) moe_int8_prepare_long_kernel(const __grid_constant__ PrepParams p) {
+  __shared__ uint32_t part[32];
   if (blockIdx.x == 0) {
-    make_schedule(p);
+    if (threadIdx.x < kPrepThreads) make_schedule(p);
     return;
   }
-  __shared__ uint32_t part[kPrepThreads / 32];
   const int64_t r = static_cast<int64_t>(blockIdx.x) - 1;
   const int64_t src = p.index != nullptr ? p.index[r] : r;
   const bool real = src >= 0 && src < p.x_rows;
   const int nvec = static_cast<int>(p.K / 8);
   const void* row = static_cast<const uint8_t*>(p.x) + (real ? src : 0) * p.K * (BF16 ? 2 : 4);
-  constexpr int KEEP = MAXV > 0 ? MAXV : 1;
-  float f[KEEP][8];
   uint32_t top_bits = 0;
-  if (real) {
-    if (MAXV > 0) {
-#pragma unroll
-      for (int i = 0; i < KEEP; ++i) {
-        const int v = threadIdx.x + i * kPrepThreads;
-        if (v < nvec) load8<BF16>(row, v, f[i]);
-      }
-    }
-    for (int i = 0; i * kPrepThreads < nvec; ++i) {
-      const int v = threadIdx.x + i * kPrepThreads;
-      if (MAXV == 0) {
-        if (v < nvec) load8<BF16>(row, v, f[0]);
-      } else if (i > 0) {
-        break;
-      }
-#pragma unroll
-      for (int m = 0; m < KEEP; ++m)
-        if (v + m * kPrepThreads < nvec && (MAXV > 0 || m == 0)) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) top_bits = max(top_bits, __float_as_uint(f[m][j]) & 0x7fffffffu);
-        }
-    }
-  }
-  top_bits = __reduce_max_sync(0xffffffffu, top_bits);
+  if (real)
+    for (int v = threadIdx.x; v < nvec; v += kPrepCta) largest<BF16>(load_raw<BF16>(row, v), top_bits);
+  top_bits = __reduce_max_sync(0xffffffffu, largest_bits<BF16>(top_bits));
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top_bits;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kPrepThreads / 32; ++w) top_bits = max(top_bits, part[w]);
-  const float top = __uint_as_float(top_bits);
-  const bool finite = top_bits < 0x7f800000u;
-  const bool zero = !finite || top_bits == 0;  // q = 0; a = NaN or 0
-  const float rcp = zero ? 0.0f : 127.0f / top;
-  if (threadIdx.x == 0) p.a[r] = finite ? top / 127.0f : __uint_as_float(0x7fc00000u);
+  top_bits = __reduce_max_sync(0xffffffffu, part[threadIdx.x % 32]);
+  const RowScale rs(top_bits);
+  if (threadIdx.x == 0) p.a[r] = row_step(top_bits);
   uint2* dst = reinterpret_cast<uint2*>(p.q + r * p.K);
-  auto emit = [&](int v, const float (&g)[8]) {
-    uint32_t w[2] = {0, 0};
-    if (!zero) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        w[j / 4] |= static_cast<uint32_t>(quantise(g[j], rcp, top) & 0xff) << (8 * (j % 4));
-    }
-    dst[v] = make_uint2(w[0], w[1]);
-  };
-  if (MAXV > 0) {
-#pragma unroll
-    for (int i = 0; i < KEEP; ++i) {
-      const int v = threadIdx.x + i * kPrepThreads;
-      if (v < nvec) emit(v, f[i]);
-    }
-  } else {
-    for (int v = threadIdx.x; v < nvec; v += kPrepThreads) {
-      if (real) load8<BF16>(row, v, f[0]);
-      emit(v, f[0]);
-    }
-  }
+  for (int v = threadIdx.x; v < nvec; v += kPrepCta)
+    dst[v] = quantise8<BF16>(load_raw<BF16>(row, v), rs);
 }
 
 // ---------------------------------------------------------------- product --
@@ -1025,14 +1199,31 @@ cudaError_t launch_pair(const moe_int8_args_t* a, const void* q, Params p, cudaS
   return cudaLaunchKernelEx(&cfg, kern, tx, tw0, tw1, p);
 }
 
+template <bool BF16, int NT>
+cudaError_t launch_prepare_ring(const PrepParams& p, int32_t ring, cudaStream_t s) {
+  auto kern = moe_int8_prepare_kernel<BF16, NT>;
+  const cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), kRingBytes);
+  if (err != cudaSuccess) return err;
+  const size_t smem = p.quantise ? static_cast<size_t>(kPrepCta / NT) * ring * p.K * (BF16 ? 2 : 4) : 0;
+  const int64_t grid = p.quantise ? std::min<int64_t>(p.R, device_sm_count()) : 1;
+  kern<<<static_cast<unsigned>(grid), kPrepCta, smem, s>>>(p, ring);
+  return cudaGetLastError();
+}
+
+// Threads per row: the fewest whose registers hold it (a warp for K <= 1024, 256
+// threads for K <= 8192), as long as two rows of every group fit in shared memory.
 template <bool BF16>
 cudaError_t launch_prepare(const PrepParams& p, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(1 + (p.quantise ? p.R : 0));
-  const int64_t vec = (p.K / 8 + kPrepThreads - 1) / kPrepThreads;  // 8-value vectors per thread
-  if (vec <= 1) moe_int8_prepare_kernel<BF16, 1><<<grid, kPrepThreads, 0, s>>>(p);
-  else if (vec <= 4) moe_int8_prepare_kernel<BF16, 4><<<grid, kPrepThreads, 0, s>>>(p);
-  else if (vec <= 16) moe_int8_prepare_kernel<BF16, 16><<<grid, kPrepThreads, 0, s>>>(p);
-  else moe_int8_prepare_kernel<BF16, 0><<<grid, kPrepThreads, 0, s>>>(p);
+  auto ring = [&](int nt) -> int32_t {
+    if (p.K > static_cast<int64_t>(nt) * 8 * kPrepVec) return 0;
+    const int64_t rows = kRingBytes / (p.K * (BF16 ? 2 : 4)) / (kPrepCta / nt);
+    return rows < 2 ? 0 : static_cast<int32_t>(std::min<int64_t>(rows, kRing));
+  };
+  if (!p.quantise) return launch_prepare_ring<BF16, 1024>(p, 0, s);
+  if (const int32_t n = ring(32)) return launch_prepare_ring<BF16, 32>(p, n, s);
+  if (const int32_t n = ring(256)) return launch_prepare_ring<BF16, 256>(p, n, s);
+  if (const int32_t n = ring(1024)) return launch_prepare_ring<BF16, 1024>(p, n, s);
+  moe_int8_prepare_long_kernel<BF16><<<static_cast<unsigned>(1 + p.R), kPrepCta, 0, s>>>(p);
   return cudaGetLastError();
 }
 
