@@ -4,15 +4,21 @@
 // One warp takes one token. Lane L holds the logits of the experts L * VPL ..
 // L * VPL + VPL - 1 (VPL = E / 32 rounded up to a power of two), so that a group of
 // experts is a run of lanes and "the lower expert" is the lower lane, then the
-// lower register. The k choices are k rounds of a warp maximum.
+// lower register.
 //
-// The choice is that of the 64-bit values. Without a bias the rank value is the
-// logit itself and every comparison is exact. With one it is score + bias, whose
-// fp32 value is off by at most `err` (derived at rank_error); a round whose winner
-// is less than 2 err ahead of the next value, or a group limit that close, is
-// undecided, and that token is chosen again from 64-bit values. With normal logits
-// that is about one token in five hundred, so the 64-bit pass costs nothing next
-// to evaluating every score in it.
+// Bound by instructions, not by the logits' bytes (16384 tokens x 256 experts: 16.8 MB,
+// 2.6 us at the copy rate), so the common path is built of few of them. A rank value
+// becomes a 32-bit key that sorts like it (as an unsigned number), whose lowest
+// log2(VPL) bits are replaced by the register index. Each lane sorts its keys once
+// (VPL <= 8), and each of the k rounds is one redux of the lanes' first keys, one ballot
+// for the lowest lane that holds it, and a shift in that lane.
+//
+// The choice is that of the 64-bit values. What a key may be off by is known (`err`: the
+// bits given to the index, and with a bias the fp32 rounding of score + bias, derived
+// at score_error); a round whose winner is less than 2 err ahead of the next value, or
+// a group limit that close, is undecided, and that token is chosen again from
+// 64-bit values. With normal logits that is about one token in a hundred. Logits of
+// few mantissa bits (bf16 ones) lose nothing to the index and are decided exactly.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -22,11 +28,11 @@
 #include <cstdint>
 
 #include "moe_internal.cuh"
+#include "sm100.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTopkWarps = 16;      // warps of a routing CTA
 constexpr int kTopkBlock = 32;      // tokens of a routing CTA: one bit each of a 32-bit mask per expert
 constexpr int kMaxExperts = 1024;
 constexpr unsigned kFull = 0xffffffffu;
@@ -37,11 +43,12 @@ struct TopkParams {
   const int32_t* n_tokens;
   int64_t T;
   int32_t E, k, n_groups, topk_groups, group_size, score, rule, renorm;
+  int32_t lane_run;     // lanes per group if that is a whole power of two, else 0
   float scale;
   int32_t* idx;
   float* weights;
   float* scores;
-  // dispatch (counts == nullptr: none)
+  // dispatch (counts == nullptr: none); hist, totals and status with more than kClusterBlocks blocks
   int32_t* counts;
   int32_t* offsets;
   int32_t* perm_token;
@@ -60,8 +67,9 @@ __device__ __forceinline__ int64_t token_count(const TopkParams& p) {
   return n < 0 ? 0 : (n < p.T ? n : p.T);
 }
 
-// fp32 value of a logit as the routing sees it: NaN masks, +inf is the largest.
-__device__ __forceinline__ float clean(float l) { return l != l ? -INFINITY : fminf(l, FLT_MAX); }
+// fp32 value of a logit as the routing sees it: NaN masks (the maximum of NaN and a
+// number is the number), +inf is the largest.
+__device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* logits, int64_t at) {
@@ -106,19 +114,31 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t t, int E, i
   }
 }
 
+// Biases of this lane's experts (0 past the last one).
+template <int VPL>
+__device__ __forceinline__ void load_bias(const float* bias, int E, int lane, float (&b)[VPL]) {
+  const int e0 = lane * VPL;
+  if (VPL >= 4 && E % 4 == 0) {
+#pragma unroll
+    for (int v = 0; v < VPL / 4; ++v)
+      if (e0 + 4 * v < E) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(bias + e0) + v);
+        b[(4 * v) % VPL] = f.x;
+        b[(4 * v + 1) % VPL] = f.y;
+        b[(4 * v + 2) % VPL] = f.z;
+        b[(4 * v + 3) % VPL] = f.w;
+      }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (e0 + j < E) b[j] = __ldg(bias + e0 + j);
+  }
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
   return v;
-}
-__device__ __forceinline__ double warp_max(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(kFull, v, o));
-  return v;
-}
-template <typename V>
-__device__ __forceinline__ V warp_min(V v) {
-  return -warp_max(-v);
 }
 template <typename V>
 __device__ __forceinline__ V warp_add(V v) {
@@ -127,306 +147,530 @@ __device__ __forceinline__ V warp_add(V v) {
   return v;
 }
 
-__device__ __forceinline__ float exp_of(float x) { return expf(x); }
-__device__ __forceinline__ double exp_of(double x) { return exp(x); }
-
-template <typename V>
-__device__ __forceinline__ V sigmoid(V l) {
-  return V(1) / (V(1) + exp_of(-l));
+// 2^x within 2 ulp and 1 / x within 1 ulp, results below the normal range as zero.
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-
-template <typename V>
-__device__ __forceinline__ V lowest() {
-  return static_cast<V>(-INFINITY);
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+constexpr float kLog2e = 1.4426950408889634f;
 
-// Order-preserving map of floats to unsigned: one redux instruction finds a warp's
-// maximum. -0 and +0 are made one first, so that they tie.
+__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+// Order-preserving map of floats to unsigned and back. -0 and +0 are made one first,
+// so that they tie.
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
+constexpr uint32_t kNoKey = 0;
+// Keys of finite and infinite values start here; smaller ones (-inf, or cleared) stand
+// for experts that cannot be chosen.
+constexpr uint32_t kFirstKey = 0x00800000u;
 
-// The warp's largest value and the lowest lane that holds it.
-__device__ __forceinline__ float warp_best(float v, int& src) {
-  const uint32_t key = order_key(v), m = __reduce_max_sync(kFull, key);
-  src = __ffs(__ballot_sync(kFull, key == m)) - 1;
-  return key_value(m);
-}
-__device__ __forceinline__ double warp_best(double v, int& src) {
-  const double m = warp_max(v);
-  src = __ffs(__ballot_sync(kFull, v == m)) - 1;
-  return m;
+// Register j of an array, j not a constant (the array stays in registers).
+template <int VPL>
+__device__ __forceinline__ float pick_reg(const float (&a)[VPL], int j) {
+  float v = a[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i)
+    if (i == j) v = a[i];
+  return v;
 }
 
-// Two largest values of a set, held as (a >= b).
-template <typename V>
-__device__ __forceinline__ void push2(V& a, V& b, V v) {
-  if (v > a) {
-    b = a;
-    a = v;
-  } else if (v > b) {
-    b = v;
+// ---- common path: 32-bit keys ------------------------------------------------
+
+// Largest first.
+template <int VPL>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[VPL]) {
+  auto order = [&](int i, int j) {
+    const uint32_t hi = max(k[i], k[j]), lo = min(k[i], k[j]);
+    k[i] = hi;
+    k[j] = lo;
+  };
+  if constexpr (VPL == 2) {
+    order(0, 1);
+  } else if constexpr (VPL == 4) {
+    order(0, 1); order(2, 3); order(0, 2); order(1, 3); order(1, 2);
+  } else if constexpr (VPL == 8) {  // odd-even merges of sorted halves
+    order(0, 1); order(2, 3); order(4, 5); order(6, 7);
+    order(0, 2); order(1, 3); order(4, 6); order(5, 7);
+    order(1, 2); order(5, 6);
+    order(0, 4); order(1, 5); order(2, 6); order(3, 7);
+    order(2, 4); order(3, 5);
+    order(1, 2); order(3, 4); order(5, 6);
   }
 }
 
-// Mask of the groups that stay. `err`: what a value may be off by (0 = exact);
-// undecided is set when two groups on either side of the limit are closer than
-// their errors allow to tell apart. rank: the values the choice goes by;
-// value: score + bias (the sum rule's terms).
-template <typename V, int VPL>
-__device__ __forceinline__ unsigned kept_groups(const TopkParams& p, int lane, const V (&rank)[VPL],
-                                                const V (&value)[VPL], V err, bool& undecided) {
+// Two largest of two such pairs (a >= b, c >= d).
+__device__ __forceinline__ void merge2(uint32_t& a, uint32_t& b, uint32_t c, uint32_t d) {
+  b = max(min(a, c), max(b, d));
+  a = max(a, c);
+}
+
+// Value of a key without its index bits, and what that may differ from the value the key
+// was made of, in units of its magnitude: VPL - 1 steps of at most 2^-23, half a step
+// for the addition of a bias and half for the sum of two.
+template <int VPL>
+__device__ __forceinline__ float bare_value(uint32_t k) {
+  return key_value(k & ~static_cast<uint32_t>(VPL - 1));
+}
+template <int VPL>
+__device__ constexpr float key_slack() {
+  return 1.2e-7f * VPL + 1.2e-7f;
+}
+
+// Bits of the leaders of the groups that stay (lane g for group g, or the first lane of
+// its run where groups are whole runs of lanes), from the keys the groups go by.
+// `undecided` is set when two groups on either side of the limit are closer than
+// their errors.
+template <int VPL>
+__device__ __forceinline__ unsigned kept_groups(const TopkParams& p, int lane, const uint32_t (&key)[VPL],
+                                                float err, bool& undecided) {
+  constexpr bool kSorted = VPL <= 8;
   const int gs = p.group_size, G = p.n_groups;
   const bool sum = p.rule == MOE_GROUP_TOP2_SUM;
-  V mine = lowest<V>();  // lane g: value of group g
-  const int run = gs / VPL;
-  if (gs % VPL == 0 && (run & (run - 1)) == 0) {
-    // a group is `run` whole lanes, a power of two: reduce within the run
-    V a = lowest<V>(), b = lowest<V>();
+  uint32_t a = kNoKey, b = kNoKey;  // leaders: the two largest keys of the group
+  bool leader = lane < G;
+  if (p.lane_run > 0) {
+    // a group is a run of whole lanes, a power of two of them: reduce within the run
+    if (kSorted) {
+      a = key[0];
+      b = VPL > 1 ? key[VPL > 1 ? 1 : 0] : kNoKey;
+    } else {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) push2(a, b, rank[j] == lowest<V>() ? lowest<V>() : (sum ? value[j] : rank[j]));
-    for (int o = 1; o < run; o <<= 1) {
-      const V a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
-      push2(a, b, a2);
-      push2(a, b, b2);
+      for (int j = 0; j < VPL; ++j) merge2(a, b, key[j], kNoKey);
     }
-    const V gv = sum && b != lowest<V>() ? a + b : a;
-    const V got = __shfl_sync(kFull, gv, (lane * run) & 31);
-    if (lane < G) mine = got;
+    for (int o = 1; o < p.lane_run; o <<= 1) {
+      const uint32_t c = __shfl_xor_sync(kFull, a, o), d = __shfl_xor_sync(kFull, b, o);
+      merge2(a, b, c, d);
+    }
+    leader = (lane & (p.lane_run - 1)) == 0 && lane < G * p.lane_run;
   } else {
     for (int g = 0; g < G; ++g) {
-      V a = lowest<V>(), b = lowest<V>();
+      uint32_t c = kNoKey, d = kNoKey;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        const int e = lane * VPL + j;
-        if (e / gs == g && rank[j] != lowest<V>()) push2(a, b, sum ? value[j] : rank[j]);
+        // the register a key came from: its own place, or its index bits once sorted
+        const int e = lane * VPL + (kSorted ? VPL - 1 - static_cast<int>(key[j] & (VPL - 1)) : j);
+        if (e / gs == g) merge2(c, d, key[j], kNoKey);
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const V a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
-        push2(a, b, a2);
-        push2(a, b, b2);
+        const uint32_t c2 = __shfl_xor_sync(kFull, c, o), d2 = __shfl_xor_sync(kFull, d, o);
+        merge2(c, d, c2, d2);
       }
-      if (lane == g) mine = sum && b != lowest<V>() ? a + b : a;
+      if (lane == g) {
+        a = c;
+        b = d;
+      }
     }
   }
-  int before = 0;  // groups ahead of this one
-  for (int g = 0; g < G; ++g) {
-    const V o = __shfl_sync(kFull, mine, g);
-    before += (o > mine || (o == mine && g < lane)) ? 1 : 0;
+  float mine = -INFINITY, size = 0.0f;  // the group's value, and the magnitude its error goes by
+  if (a >= kFirstKey) {
+    mine = bare_value<VPL>(a);
+    size = fabsf(mine);
+    if (sum && b >= kFirstKey) {
+      const float second = bare_value<VPL>(b);
+      mine += second;
+      size += fabsf(second);
+    }
   }
-  const bool keep = lane < G && before < p.topk_groups;
-  const unsigned mask = __ballot_sync(kFull, keep);
-  if (err > V(0) && p.topk_groups < G) {
-    const V low = warp_min(keep ? mine : static_cast<V>(INFINITY));
-    const V high = warp_max(lane < G && !keep ? mine : lowest<V>());
-    // two values of `err` each in a sum, on both sides; empty groups are exact
-    if (high > lowest<V>() && !(low - high > V(4) * err)) undecided = true;
+  if (__any_sync(kFull, leader && mine != mine)) undecided = true;  // infinite biases
+  // largest first, the lower group among equal ones; + 1: an empty group is above no group
+  uint32_t left = leader ? order_key(mine) + 1 : 0;
+  unsigned kept = 0;
+  int src = 0;
+  for (int i = 0; i < p.topk_groups; ++i) {
+    src = __ffs(__ballot_sync(kFull, left == __reduce_max_sync(kFull, left))) - 1;
+    kept |= 1u << src;
+    if (lane == src) left = 0;
   }
-  return mask;
+  if (p.topk_groups < G && err >= 0.0f) {
+    // the worst of those that stay against the best of those that go
+    const int next = __ffs(__ballot_sync(kFull, left == __reduce_max_sync(kFull, left))) - 1;
+    const float low = __shfl_sync(kFull, mine, src), high = __shfl_sync(kFull, mine, next);
+    const float sizes = __shfl_sync(kFull, size, src) + __shfl_sync(kFull, size, next);
+    // an empty group is exact
+    if (high != -INFINITY && !(low - high > 4.0f * err + key_slack<VPL>() * sizes)) undecided = true;
+  }
+  return kept;
 }
 
-// k rounds of the warp's largest rank value, dropped as they are taken. Lane i
-// ends with the i-th choice in `pick` (-1: none left). With err > 0 one more
-// round looks at the value behind the last, and `undecided` is set when two
-// neighbours are closer than 2 err.
-template <typename V, int VPL>
-__device__ __forceinline__ void take_k(V (&rank)[VPL], int k, int lane, V err, bool& undecided, int& pick) {
-  pick = -1;
-  V best = lowest<V>();
-  int at = 0;
+// k rounds of the warp's largest key. Lane i ends with the i-th choice in `pick` (-1:
+// none left); one more round looks at the value behind the last. `err` < 0: the
+// keys lost nothing, every comparison is exact.
+template <int VPL>
+__device__ __forceinline__ void take_k(uint32_t (&key)[VPL], int k, int lane, float err, bool& undecided, int& pick) {
+  constexpr bool kSorted = VPL <= 8;
+  constexpr uint32_t kIndex = VPL - 1;
+  uint32_t best = key[0], mine = kNoKey;
+  if (!kSorted) {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j)
-    if (rank[j] > best) {
-      best = rank[j];
-      at = j;
-    }
-  V last = static_cast<V>(INFINITY);
-  const int rounds = err > V(0) ? k + 1 : k;
+    for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
+  }
+  int from = 0;
+  const int rounds = err >= 0.0f ? min(k + 1, 32) : k;
   for (int i = 0; i < rounds; ++i) {
-    int src;
-    const V m = warp_best(best, src);
-    if (m == lowest<V>()) break;
-    if (err > V(0) && i > 0 && !(last - m > V(2) * err)) undecided = true;
-    last = m;
-    if (i == k) break;
-    const int e = __shfl_sync(kFull, lane * VPL + at, src);
-    if (lane == i) pick = e;
-    if (lane == src) {
-      best = lowest<V>();
-      int next = 0;
+    // the values alone decide; among equal ones the lowest lane, in it the lowest register
+    const uint32_t head = best | kIndex;
+    const uint32_t m = __reduce_max_sync(kFull, head);
+    if (m < kFirstKey) break;
+    const int src = __ffs(__ballot_sync(kFull, head == m)) - 1;
+    const uint32_t full = __shfl_sync(kFull, best, src);
+    mine = lane == i ? full : mine;
+    from = lane == i ? src : from;
+    const bool own = lane == src;
+    if (kSorted) {
+#pragma unroll
+      for (int j = 0; j + 1 < VPL; ++j) key[j] = own ? key[j + 1] : key[j];
+      key[VPL - 1] = own ? kNoKey : key[VPL - 1];
+      best = key[0];
+    } else if (own) {
+      best = kNoKey;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        if (j == at) rank[j] = lowest<V>();
-        if (rank[j] > best) {
-          best = rank[j];
-          next = j;
-        }
+        if (key[j] == full) key[j] = kNoKey;
+        best = max(best, key[j]);
       }
-      at = next;
     }
   }
+  pick = lane < k && mine >= kFirstKey ? from * VPL + (VPL - 1 - static_cast<int>(mine & (VPL - 1))) : -1;
+  if (err >= 0.0f) {
+    // neighbours closer than both may be off: the fp32 error and the index bits
+    const uint32_t next = __shfl_down_sync(kFull, mine, 1);
+    const float a = key_value(mine), b = key_value(next);
+    const float e = 2.0f * err + key_slack<VPL>() * (fabsf(a) + fabsf(b));
+    const bool close = lane < 31 && next >= kFirstKey && !(a - b > e);
+    // with k = 32 there is no lane for the value behind the last: never decided here
+    if (__any_sync(kFull, close) || k == 32) undecided = true;
+  }
+}
+
+// ---- 64-bit values -------------------------------------------------------------
+// The same steps on 64-bit keys that sort like doubles. One such token can be the last
+// of its kernel, so its own time counts: 16384 tokens of 256 experts took 16 us longer
+// when every round was a shuffle reduction of doubles.
+
+__device__ __forceinline__ uint64_t order_key64(double v) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+  return b ^ (static_cast<uint64_t>(static_cast<int64_t>(b) >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double key_value64(uint64_t k) {
+  return __longlong_as_double(
+      static_cast<long long>(k & 0x8000000000000000ull ? k ^ 0x8000000000000000ull : ~k));
+}
+constexpr uint64_t kFirstKey64 = 0x0010000000000000ull;  // below: -inf, or no value
+
+// The warp's largest key (0 = none) and the lowest lane that holds it.
+__device__ __forceinline__ uint64_t warp_best64(uint64_t k, int& src) {
+  const uint32_t hi = static_cast<uint32_t>(k >> 32);
+  const uint32_t mh = __reduce_max_sync(kFull, hi);
+  const uint32_t lo = hi == mh ? static_cast<uint32_t>(k) : 0;
+  const uint32_t ml = __reduce_max_sync(kFull, lo);
+  src = __ffs(__ballot_sync(kFull, hi == mh && static_cast<uint32_t>(k) == ml)) - 1;
+  return static_cast<uint64_t>(mh) << 32 | ml;
+}
+
+// Two largest of a set, held as (a >= b).
+__device__ __forceinline__ void push2(uint64_t& a, uint64_t& b, uint64_t v) {
+  b = max(b, min(a, v));
+  a = max(a, v);
+}
+
+// Bits of the leaders of the groups that stay (see kept_groups).
+template <int VPL>
+__device__ __forceinline__ unsigned kept_groups_exact(const TopkParams& p, int lane, const uint64_t (&key)[VPL]) {
+  const int G = p.n_groups;
+  uint64_t a = 0, b = 0;
+  bool leader = lane < G;
+  if (p.lane_run > 0) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) push2(a, b, key[j]);
+    for (int o = 1; o < p.lane_run; o <<= 1) {
+      const uint64_t c = __shfl_xor_sync(kFull, a, o), d = __shfl_xor_sync(kFull, b, o);
+      push2(a, b, c);
+      push2(a, b, d);
+    }
+    leader = (lane & (p.lane_run - 1)) == 0 && lane < G * p.lane_run;
+  } else {
+    for (int g = 0; g < G; ++g) {
+      uint64_t c = 0, d = 0;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if ((lane * VPL + j) / p.group_size == g) push2(c, d, key[j]);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t c2 = __shfl_xor_sync(kFull, c, o), d2 = __shfl_xor_sync(kFull, d, o);
+        push2(c, d, c2);
+        push2(c, d, d2);
+      }
+      if (lane == g) {
+        a = c;
+        b = d;
+      }
+    }
+  }
+  double mine = -INFINITY;
+  if (a >= kFirstKey64) {
+    mine = key_value64(a);
+    if (p.rule == MOE_GROUP_TOP2_SUM && b >= kFirstKey64) mine += key_value64(b);
+  }
+  uint64_t left = leader ? order_key64(mine) + 1 : 0;  // an empty group is above no group
+  unsigned kept = 0;
+  for (int i = 0; i < p.topk_groups; ++i) {
+    int src;
+    warp_best64(left, src);
+    kept |= 1u << src;
+    if (lane == src) left = 0;
+  }
+  return kept;
+}
+
+template <int VPL>
+__device__ __forceinline__ int take_k_exact(uint64_t (&key)[VPL], int k, int lane) {
+  int pick = -1;
+  for (int i = 0; i < k; ++i) {
+    uint64_t best = key[0];
+    int at = 0;
+#pragma unroll
+    for (int j = 1; j < VPL; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = j;
+      }
+    int src;
+    if (warp_best64(best, src) < kFirstKey64) break;
+    const int e = __shfl_sync(kFull, lane * VPL + at, src);
+    if (lane == i) pick = e;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (lane == src && j == at) key[j] = 0;
+  }
+  return pick;
 }
 
 // Scores of this lane's experts, the row's largest logit and, for softmax, the sum.
-template <typename V, int VPL>
-__device__ __forceinline__ void row_scores(int score, const float (&l)[VPL], V (&s)[VPL], float& top, V& z) {
+template <int VPL>
+__device__ __forceinline__ void row_scores(int score, const float (&l)[VPL], float (&s)[VPL], float& top, float& z) {
   top = -INFINITY;
-  z = V(1);
+  z = 1.0f;
   if (score == MOE_SCORE_SIGMOID) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) s[j] = l[j] == -INFINITY ? V(0) : sigmoid(static_cast<V>(l[j]));
+    for (int j = 0; j < VPL; ++j) s[j] = l[j] == -INFINITY ? 0.0f : sigmoid(l[j]);
     return;
   }
 #pragma unroll
   for (int j = 0; j < VPL; ++j) top = fmaxf(top, l[j]);
   top = warp_max(top);
-  V sum = V(0);
+  float sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    s[j] = l[j] == -INFINITY ? V(0) : exp_of(static_cast<V>(l[j]) - static_cast<V>(top));
+    s[j] = l[j] == -INFINITY ? 0.0f : expf(l[j] - top);
     sum += s[j];
   }
   z = warp_add(sum);
-  if (!(z > V(0))) z = V(1);
+  if (!(z > 0.0f)) z = 1.0f;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) s[j] /= z;
 }
 
-// What an fp32 score + bias may be off by from its 64-bit value, with u = 2^-24.
-// Sigmoid: expf is within 2 u of relative error, the sum and the division add u each,
-// and d s / d(e^-l) shrinks the first: at most 5 u s <= 3e-7. Softmax: the difference
-// l - max is rounded (|l - max| u in the exponent, at most 0.37 u next to the largest
-// term once multiplied by e^(l - max)), expf 2 u, and the sum of E <= 1024 terms in 32
-// rounds and 5 levels 37 u more, the division u: at most 45 u s <= 2.7e-6 s. The
-// addition of the bias: u |s + b|.
-__device__ __forceinline__ float rank_error(int score, float s_top, float c_top) {
-  return (score == MOE_SCORE_SIGMOID ? 3.6e-7f : 3.0e-6f) * s_top + 1.2e-7f * c_top;
-}
-
-template <bool BF16, int VPL, typename V>
-__device__ __forceinline__ void rank_values(const TopkParams& p, int lane, const float (&l)[VPL], const V (&s)[VPL],
-                                            V (&rank)[VPL], V (&value)[VPL]) {
+// Scores for the ranking alone: approximate exponential and quotient (written scores and
+// weights use accurate ones), and for softmax the largest logit and the sum.
+template <int VPL>
+__device__ __forceinline__ void rank_scores(int score, const float (&l)[VPL], float (&s)[VPL], float& s_top,
+                                            float& top, float& z) {
+  if (score == MOE_SCORE_SIGMOID) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) s[j] = rcp_fast(1.0f + ex2_fast(-kLog2e * l[j]));
+    s_top = 1.0f;
+    return;
+  }
+  top = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) top = fmaxf(top, l[j]);
+  top = key_value(__reduce_max_sync(kFull, order_key(top)));
+  float sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    const int e = lane * VPL + j;
-    value[j] = s[j];
-    rank[j] = static_cast<V>(l[j]);
-    if (p.bias != nullptr && e < p.E) {
-      value[j] = s[j] + static_cast<V>(__ldg(p.bias + e));
-      rank[j] = l[j] == -INFINITY || value[j] != value[j] ? lowest<V>() : value[j];
-    }
+    s[j] = l[j] == -INFINITY ? 0.0f : ex2_fast(kLog2e * (l[j] - top));
+    sum += s[j];
   }
+  z = warp_add(sum);
+  if (!(z > 0.0f)) z = 1.0f;
+  s_top = rcp_fast(z);
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) s[j] *= s_top;
 }
 
-template <typename V, int VPL>
-__device__ __forceinline__ void choose(const TopkParams& p, int lane, V (&rank)[VPL], const V (&value)[VPL],
-                                       V group_err, V err, bool& undecided, int& pick) {
-  if (p.n_groups > 1) {
-    const unsigned kept = kept_groups<V, VPL>(p, lane, rank, value, group_err, undecided);
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int g = (lane * VPL + j) / p.group_size;
-      if (g >= 32 || !((kept >> g) & 1u)) rank[j] = lowest<V>();
-    }
-  }
-  take_k<V, VPL>(rank, p.k, lane, err, undecided, pick);
+// What rank_scores may be off by, with u = 2^-24. 2^(x log2 e): the product's rounding
+// and log2 e's own count 2 |x| u in the exponent, ex2 2 ulp (4 u). Sigmoid, x = -l: s =
+// 1 / (1 + e^x), so a relative error d of the exponential is s (1 - s) d absolute; with
+// s (1 - s) <= 0.25 and |x| s (1 - s) <= 0.23 at most (0.46 + 1) u, plus sum u and
+// reciprocal 2 u: below 5 u; scores that e^x > 2^126 flushes to zero are below 2^-126.
+// Softmax, x = l - max <= 0, itself rounded by |x| u: |x| e^x <= 0.37, so a term is off by
+// at most 3 * 0.37 + 4 < 6 u of the largest term, the sum of 1024 terms by that and
+// 37 u, reciprocal 2 u, product u: 46 u of the largest score. The addition of the bias:
+// u |c|, part of key_slack.
+__device__ __forceinline__ float score_error(int score, float s_top) {
+  return score == MOE_SCORE_SIGMOID ? 3.0e-7f : 3.0e-6f * s_top;
 }
 
 // The choice from 64-bit values. A call of its own: its registers are not those
 // of the common path.
 template <bool BF16, int VPL>
 __device__ __noinline__ int choose_exact(const TopkParams& p, int64_t t, int lane) {
+  const bool biased = p.bias != nullptr, sums = p.n_groups > 1 && p.rule == MOE_GROUP_TOP2_SUM;
   float l[VPL];
   load_row<BF16, VPL>(p.logits, t, p.E, lane, l);
-  double s[VPL], rank[VPL], value[VPL], z;
-  float top;
-  row_scores<double, VPL>(p.score, l, s, top, z);
-  rank_values<BF16, VPL, double>(p, lane, l, s, rank, value);
-  bool undecided = false;
-  int pick;
-  choose<double, VPL>(p, lane, rank, value, 0.0, 0.0, undecided, pick);
-  return pick;
+  uint64_t key[VPL];
+  auto by_logit = [&] {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = order_key64(static_cast<double>(l[j]));
+  };
+  auto by_score = [&] {
+    double top = 0.0, z = 1.0;
+    if (p.score == MOE_SCORE_SOFTMAX) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) m = fmaxf(m, l[j]);
+      m = key_value(__reduce_max_sync(kFull, order_key(m)));
+      top = m > -INFINITY ? static_cast<double>(m) : 0.0;
+      z = 0.0;
+#pragma unroll 1
+      for (int j = 0; j < VPL; ++j) z += exp(static_cast<double>(pick_reg<VPL>(l, j)) - top);
+      z = warp_add(z);
+    }
+#pragma unroll 1
+    for (int j = 0; j < VPL; ++j) {
+      const float x = pick_reg<VPL>(l, j);
+      const int e = lane * VPL + j;
+      double v = p.score == MOE_SCORE_SOFTMAX ? exp(static_cast<double>(x) - top) / z
+                                              : 1.0 / (1.0 + exp(-static_cast<double>(x)));
+      if (biased && e < p.E) v += static_cast<double>(__ldg(p.bias + e));
+      const uint64_t k = x == -INFINITY || v != v ? 0 : order_key64(v);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (i == j) key[i] = k;
+    }
+  };
+  if (biased || sums) by_score();
+  else by_logit();
+  unsigned kept = kFull;
+  if (p.n_groups > 1) kept = kept_groups_exact<VPL>(p, lane, key);
+  if (sums && !biased) by_logit();
+  if (p.n_groups > 1) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int g = p.lane_run > 0 ? lane & ~(p.lane_run - 1) : (lane * VPL + j) / p.group_size;
+      if (g >= 32 || !((kept >> g) & 1u)) key[j] = 0;
+    }
+  }
+  return take_k_exact<VPL>(key, p.k, lane);
 }
 
-// Share of each choice in the renormalised weights (lanes 0 .. k-1 hold one choice
-// with logit lv, -inf = none): s / sum s, computed from differences of logits, so
-// that scores below the fp32 range still share. Sigmoid scores of logits below -60
-// are exp(l) to 26 digits.
-__device__ __forceinline__ float share_of(int score, float lv, bool has) {
-  const float top = warp_max(has ? lv : -INFINITY);
+// Share of each choice in the renormalised weights (P lanes of a warp, a power of two,
+// hold the choices of one token; logit lv, -inf = none): s / sum s, computed from
+// differences of logits, so that scores below the fp32 range still share. Sigmoid
+// scores of logits below -60 are exp(l) to 26 digits.
+__device__ __forceinline__ float share_of(int score, float lv, int P) {
+  float top = lv;
+  for (int o = 1; o < P; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
   float x = 0.0f;
-  if (has && lv > -INFINITY) x = score == MOE_SCORE_SIGMOID && top > -60.0f ? sigmoid(lv) : expf(lv - top);
-  const float sum = warp_add(x);
+  if (lv > -INFINITY) x = score == MOE_SCORE_SIGMOID && top > -60.0f ? sigmoid(lv) : expf(lv - top);
+  float sum = x;
+  for (int o = 1; o < P; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
   return sum > 0.0f ? x / sum : 0.0f;
 }
 
-// One token by one warp: idx, weights, scores. Lane i < k ends with choice i and
-// its weight.
+// The choice of one token: lane i < k ends with choice i. For softmax weights and
+// scores also the row's largest logit and its sum.
 template <bool BF16, int VPL>
-__device__ __forceinline__ void route_token(const TopkParams& p, int64_t t, int lane, bool real, int& pick,
-                                            float& weight) {
-  pick = -1;
-  weight = 0.0f;
-  if (!real) {
-    if (p.scores != nullptr)
-      for (int e = lane; e < p.E; e += 32) p.scores[t * p.E + e] = 0.0f;
+__device__ __forceinline__ int choose(const TopkParams& p, int64_t t, int lane, float& top, float& z) {
+  float l[VPL];
+  load_row<BF16, VPL>(p.logits, t, p.E, lane, l);
+  const bool groups = p.n_groups > 1, sums = groups && p.rule == MOE_GROUP_TOP2_SUM;
+  const bool biased = p.bias != nullptr;
+  float s[VPL], s_top = 1.0f;
+  if (p.scores != nullptr) {
+    row_scores<VPL>(p.score, l, s, top, z);
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (lane * VPL + j < p.E) p.scores[t * p.E + lane * VPL + j] = s[j];
+    if (p.score == MOE_SCORE_SOFTMAX) s_top = 1.0f / z;
+  } else if (biased || sums || (p.score == MOE_SCORE_SOFTMAX && p.renorm == 0)) {
+    rank_scores<VPL>(p.score, l, s, s_top, top, z);
+  }
+  // Keys by score + bias, or by the logit; groups that sum scores without a bias go
+  // by keys of their own.
+  uint32_t key[VPL];
+  auto by_score = [&] {
+    float bias[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) bias[j] = 0.0f;
+    if (biased) load_bias<VPL>(p.bias, p.E, lane, bias);
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      // 0 * l: NaN for a masked expert; the maximum turns NaN into -inf
+      const float v = fmaxf(fmaf(l[j], 0.0f, s[j] + bias[j]), -INFINITY);
+      key[j] = (order_key(v) & ~static_cast<uint32_t>(VPL - 1)) | static_cast<uint32_t>(VPL - 1 - j);
+    }
+    if (VPL <= 8) sort_keys<VPL>(key);
+  };
+  bool undecided = false;
+  unsigned kept = kFull;
+  float err = score_error(p.score, s_top);
+  if (sums && !biased) {
+    by_score();
+    kept = kept_groups<VPL>(p, lane, key, err, undecided);
+  }
+  if (biased) {
+    by_score();
   } else {
-    float l[VPL], s[VPL], z = 1.0f, top = 0.0f;
-    load_row<BF16, VPL>(p.logits, t, p.E, lane, l);
-    const bool sums = p.n_groups > 1 && p.rule == MOE_GROUP_TOP2_SUM;
-    const bool need_all = p.bias != nullptr || p.scores != nullptr || sums ||
-                          (p.score == MOE_SCORE_SOFTMAX && p.renorm == 0);
-    if (need_all) {
-      row_scores<float, VPL>(p.score, l, s, top, z);
-    } else {
+    uint32_t lost = 0;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) s[j] = 0.0f;
+    for (int j = 0; j < VPL; ++j) {
+      lost |= __float_as_uint(l[j]);
+      key[j] = (order_key(l[j]) & ~static_cast<uint32_t>(VPL - 1)) | static_cast<uint32_t>(VPL - 1 - j);
     }
-    if (p.scores != nullptr) {
-#pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (lane * VPL + j < p.E) p.scores[t * p.E + lane * VPL + j] = s[j];
-    }
-    float rank[VPL], value[VPL];
-    rank_values<BF16, VPL, float>(p, lane, l, s, rank, value);
-    float err = 0.0f;
-    if (p.bias != nullptr || sums) {
-      float st = 0.0f, ct = 0.0f;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        st = fmaxf(st, s[j]);
-        ct = fmaxf(ct, rank[j] == -INFINITY ? 0.0f : fabsf(value[j]));
-      }
-      err = fmaxf(rank_error(p.score, warp_max(st), warp_max(ct)), FLT_MIN);
-    }
-    bool undecided = false;
-    choose<float, VPL>(p, lane, rank, value, err, p.bias != nullptr ? err : 0.0f, undecided, pick);
-    if (undecided) pick = choose_exact<BF16, VPL>(p, t, lane);  // the same on every lane
-    const bool has = pick >= 0;
-    const float lv = has ? load_logit<BF16>(p.logits, t * p.E + pick) : -INFINITY;
-    if (p.renorm) {
-      weight = share_of(p.score, lv, has);
-    } else if (has) {
-      weight = p.score == MOE_SCORE_SIGMOID ? sigmoid(lv) : expf(lv - top) / z;
-    }
-    weight *= p.scale;
+    if (VPL <= 8) sort_keys<VPL>(key);
+    // exact where no logit has a bit that the index took
+    err = VPL > 1 && __any_sync(kFull, (lost & (VPL - 1)) != 0) ? 0.0f : -1.0f;
   }
-  if (lane < p.k) {
-    p.idx[t * p.k + lane] = pick;
-    p.weights[t * p.k + lane] = weight;
+  if (groups && !(sums && !biased)) kept = kept_groups<VPL>(p, lane, key, err, undecided);
+  if (groups && p.lane_run > 0) {
+    if (!((kept >> (lane & ~(p.lane_run - 1))) & 1u)) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) key[j] = kNoKey;
+    }
+  } else if (groups) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int at = VPL <= 8 ? VPL - 1 - static_cast<int>(key[j] & (VPL - 1)) : j;
+      const int g = (lane * VPL + at) / p.group_size;
+      if (g >= 32 || !((kept >> g) & 1u)) key[j] = kNoKey;
+    }
+    if (VPL > 1 && VPL <= 8) sort_keys<VPL>(key);  // holes inside a lane
   }
+  int pick;
+  take_k<VPL>(key, p.k, lane, err, undecided, pick);
+  if (undecided) pick = choose_exact<BF16, VPL>(p, t, lane);  // the same on every lane
+  return pick;
 }
 
-// Exclusive prefix of counts[0..E) over a CTA of kTopkWarps * 32 threads, into
+// Exclusive prefix of counts[0..E) over a CTA of NW warps, into
 // pre[0..E] (shared). counts(e) is called once per expert.
-template <typename F>
+template <int NW, typename F>
 __device__ __forceinline__ void block_prefix(int E, int* pre, int* part, F counts) {
-  constexpr int NT = kTopkWarps * 32;
+  constexpr int NT = NW * 32;
   constexpr int PER = kMaxExperts / NT;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   int c[PER], sum = 0;
@@ -460,12 +704,12 @@ __device__ __forceinline__ void block_prefix(int E, int* pre, int* part, F count
 // Places of one block's slots: start(e) = first permuted row of this block's slots
 // of expert e; mask[e] = the block's tokens that chose e, so a slot's rank is the
 // number of lower bits set.
-template <typename F>
+template <int NW, typename F>
 __device__ __forceinline__ void place_slots(const TopkParams& p, int64_t blk, const uint32_t* mask, int total,
                                             F start) {
   const int64_t t0 = blk * kTopkBlock;
   const int tokens = static_cast<int>(p.T - t0 < kTopkBlock ? p.T - t0 : kTopkBlock);
-  for (int i = threadIdx.x; i < tokens * p.k; i += kTopkWarps * 32) {
+  for (int i = threadIdx.x; i < tokens * p.k; i += NW * 32) {
     const int tok = i / p.k;
     const int64_t at = t0 * p.k + i;
     const int e = p.idx[at];
@@ -485,44 +729,91 @@ __device__ __forceinline__ void place_slots(const TopkParams& p, int64_t blk, co
   }
 }
 
-// Routing of one block of kTopkBlock tokens, two per warp; with the dispatch arrays
-// also the block's slots per expert. A batch of one block is dispatched here too.
-template <bool BF16, int VPL>
-__global__ void __launch_bounds__(kTopkWarps * 32) moe_topk_route_kernel(const __grid_constant__ TopkParams p) {
+// Routing of one block of kTopkBlock tokens by NW warps: first the choices, a token per
+// warp at a time, then the weights of all tokens side by side (as many tokens per warp as
+// their choices leave room for). With the dispatch arrays also the block's slots per
+// expert; a batch of up to kClusterBlocks blocks runs as one cluster that reads those of
+// the other blocks from their shared memory and finishes the dispatch itself. Up to
+// a block per SM the tokens of a block run side by side (NW = 32, or 16 where a lane's
+// registers allow no more); with more blocks NW = 8, so that more blocks share an SM.
+constexpr int kClusterBlocks = 8;
+
+template <bool BF16, int VPL, int NW>
+__global__ void __launch_bounds__(NW * 32, VPL <= 8 ? 32 / NW : 1)
+    moe_topk_route_kernel(const __grid_constant__ TopkParams p) {
   __shared__ uint32_t mask[kMaxExperts];
   __shared__ int pre[kMaxExperts + 1];
-  __shared__ int part[kTopkWarps];
+  __shared__ int below[kMaxExperts];
+  __shared__ int part[NW];
+  __shared__ int picks[kTopkBlock][32];
+  __shared__ float tops[kTopkBlock], sums[kTopkBlock];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTopkBlock;
   const int64_t n = token_count(p);
   const bool dispatch = p.counts != nullptr;
   if (dispatch) {
-    for (int e = threadIdx.x; e < p.E; e += kTopkWarps * 32) mask[e] = 0;
+    for (int e = threadIdx.x; e < p.E; e += NW * 32) mask[e] = 0;
     __syncthreads();
   }
 #pragma unroll 1
-  for (int i = warp; i < kTopkBlock; i += kTopkWarps) {
+  for (int i = warp; i < kTopkBlock; i += NW) {
     const int64_t t = t0 + i;
     if (t >= p.T) break;
-    int pick;
-    float weight;
-    route_token<BF16, VPL>(p, t, lane, t < n, pick, weight);
+    int pick = -1;
+    if (t < n) {
+      float top = 0.0f, z = 1.0f;
+      pick = choose<BF16, VPL>(p, t, lane, top, z);
+      if (lane == 0) {
+        tops[i] = top;
+        sums[i] = z;
+      }
+    } else if (p.scores != nullptr) {
+      for (int e = lane; e < p.E; e += 32) p.scores[t * p.E + e] = 0.0f;
+    }
+    picks[i][lane] = pick;
     if (dispatch && pick >= 0) atomicOr(&mask[pick], 1u << i);
   }
-  if (!dispatch) return;
   __syncthreads();
-  if (p.nblk > 1) {
-    for (int e = threadIdx.x; e < p.E; e += kTopkWarps * 32)
+  const int P = p.k <= 1 ? 1 : 1 << (32 - __clz(p.k - 1));  // lanes of a token
+  for (int i0 = 0; i0 < kTopkBlock * P; i0 += NW * 32) {
+    const int i = i0 + threadIdx.x, tok = i / P, slot = i % P;
+    const int64_t t = t0 + tok;
+    const bool in = tok < kTopkBlock && t < p.T && slot < p.k;
+    const int pick = in ? picks[tok][slot] : -1;
+    const float lv = pick >= 0 ? load_logit<BF16>(p.logits, t * p.E + pick) : -INFINITY;
+    float w = 0.0f;
+    if (p.renorm) w = share_of(p.score, lv, P);
+    else if (pick >= 0) w = p.score == MOE_SCORE_SIGMOID ? sigmoid(lv) : expf(lv - tops[tok]) / sums[tok];
+    if (in) {
+      p.idx[t * p.k + slot] = pick;
+      p.weights[t * p.k + slot] = w * p.scale;
+    }
+  }
+  if (!dispatch) return;
+  if (p.nblk > kClusterBlocks) {
+    for (int e = threadIdx.x; e < p.E; e += NW * 32)
       p.hist[static_cast<int64_t>(blockIdx.x) * p.E + e] = __popc(mask[e]);
     return;
   }
-  block_prefix(p.E, pre, part, [&](int e) { return __popc(mask[e]); });
-  for (int e = threadIdx.x; e < p.E; e += kTopkWarps * 32) {
-    p.counts[e] = __popc(mask[e]);
-    p.offsets[e] = pre[e];
-  }
-  if (threadIdx.x == 0) p.offsets[p.E] = pre[p.E];
-  place_slots(p, 0, mask, pre[p.E], [&](int e) { return pre[e]; });
+  const int blocks = static_cast<int>(p.nblk), me = blockIdx.x;
+  if (blocks > 1) sm100::cluster_sync();  // every block's masks are complete
+  else __syncthreads();                   // idx and weights are written
+  block_prefix<NW>(p.E, pre, part, [&](int e) {
+    int all = 0, lower = 0;
+    for (int b = 0; b < blocks; ++b) {
+      const int c = __popc(b == me ? mask[e] : static_cast<uint32_t>(sm100::ld_shared_cluster_s32(
+                                                   sm100::mapa_shared(&mask[e], b))));
+      all += c;
+      lower += b < me ? c : 0;
+    }
+    below[e] = lower;
+    if (me == 0) p.counts[e] = all;
+    return all;
+  });
+  if (me == 0)
+    for (int e = threadIdx.x; e <= p.E; e += NW * 32) p.offsets[e] = pre[e];
+  place_slots<NW>(p, me, mask, pre[p.E], [&](int e) { return pre[e] + below[e]; });
+  if (blocks > 1) sm100::cluster_sync();  // no block leaves while another may read its masks
 }
 
 // Exclusive prefix over the token blocks of every expert's slots (in place), and the
@@ -535,14 +826,27 @@ __global__ void __launch_bounds__(1024) moe_topk_scan_kernel(const TopkParams p)
   const int e = blockIdx.x * 32 + x;
   const int64_t per = (p.nblk + 31) / 32, b0 = y * per, b1 = b0 + per < p.nblk ? b0 + per : p.nblk;
   int sum = 0;
-  if (e < p.E)
+  if (e < p.E) {
+#pragma unroll 8
     for (int64_t b = b0; b < b1; ++b) sum += p.hist[b * p.E + e];
+  }
   run[y][x] = sum;
   __syncthreads();
   int at = 0;
   for (int i = 0; i < y; ++i) at += run[i][x];
   if (e < p.E) {
-    for (int64_t b = b0; b < b1; ++b) {
+    int64_t b = b0;
+    for (; b + 8 <= b1; b += 8) {
+      int c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = p.hist[(b + j) * p.E + e];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p.hist[(b + j) * p.E + e] = at;
+        at += c[j];
+      }
+    }
+    for (; b < b1; ++b) {
       const int c = p.hist[b * p.E + e];
       p.hist[b * p.E + e] = at;
       at += c;
@@ -551,29 +855,31 @@ __global__ void __launch_bounds__(1024) moe_topk_scan_kernel(const TopkParams p)
   }
 }
 
+constexpr int kDispatchWarps = 8;
+
 // Dispatch of one token block after the scan.
-__global__ void __launch_bounds__(kTopkWarps * 32) moe_topk_dispatch_kernel(const TopkParams p) {
+__global__ void __launch_bounds__(kDispatchWarps * 32) moe_topk_dispatch_kernel(const TopkParams p) {
   __shared__ uint32_t mask[kMaxExperts];
   __shared__ int pre[kMaxExperts + 1];
-  __shared__ int part[kTopkWarps];
+  __shared__ int part[kDispatchWarps];
   const int64_t blk = blockIdx.x;
-  for (int e = threadIdx.x; e < p.E; e += kTopkWarps * 32) mask[e] = 0;
-  block_prefix(p.E, pre, part, [&](int e) { return p.totals[e]; });
+  for (int e = threadIdx.x; e < p.E; e += kDispatchWarps * 32) mask[e] = 0;
+  block_prefix<kDispatchWarps>(p.E, pre, part, [&](int e) { return p.totals[e]; });
   const int64_t t0 = blk * kTopkBlock;
   const int tokens = static_cast<int>(p.T - t0 < kTopkBlock ? p.T - t0 : kTopkBlock);
-  for (int i = threadIdx.x; i < tokens * p.k; i += kTopkWarps * 32) {
+  for (int i = threadIdx.x; i < tokens * p.k; i += kDispatchWarps * 32) {
     const int e = p.idx[t0 * p.k + i];
     if (e >= 0) atomicOr(&mask[e], 1u << (i / p.k));
   }
   __syncthreads();
   if (blk == 0) {
-    for (int e = threadIdx.x; e < p.E; e += kTopkWarps * 32) {
+    for (int e = threadIdx.x; e < p.E; e += kDispatchWarps * 32) {
       p.counts[e] = p.totals[e];
       p.offsets[e] = pre[e];
     }
     if (threadIdx.x == 0) p.offsets[p.E] = pre[p.E];
   }
-  place_slots(p, blk, mask, pre[p.E], [&](int e) { return pre[e] + p.hist[blk * p.E + e]; });
+  place_slots<kDispatchWarps>(p, blk, mask, pre[p.E], [&](int e) { return pre[e] + p.hist[blk * p.E + e]; });
 }
 
 // ------------------------------------------------------------- backward --
@@ -595,10 +901,17 @@ struct TopkGradParams {
   float scale;
 };
 
+constexpr int kGradWarps = 8;
+
+// One token per warp. The chosen experts' terms reach their lanes through a row of
+// shared memory: plain stores where the choice names no expert twice, else one after
+// the other in slot order.
 template <bool BF16, int VPL>
-__global__ void __launch_bounds__(256) moe_topk_grad_kernel(const __grid_constant__ TopkGradParams p) {
+__global__ void __launch_bounds__(kGradWarps * 32) moe_topk_grad_kernel(const __grid_constant__ TopkGradParams p) {
+  __shared__ __align__(16) float rows[kGradWarps][32 * VPL];
   const int lane = threadIdx.x % 32;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+  float* chosen = rows[threadIdx.x / 32];
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kGradWarps + threadIdx.x / 32;
   if (t >= p.T) return;
   int64_t n = p.T;
   if (p.n_tokens != nullptr) n = __ldg(p.n_tokens);
@@ -606,9 +919,6 @@ __global__ void __launch_bounds__(256) moe_topk_grad_kernel(const __grid_constan
 #pragma unroll
   for (int j = 0; j < VPL; ++j) d[j] = 0.0f;
   if (t < n) {
-    float l[VPL], s[VPL], z, top;
-    load_row<BF16, VPL>(p.logits, t, p.E, lane, l);
-    row_scores<float, VPL>(p.score, l, s, top, z);
     int pick = -1;
     float g = 0.0f, lv = -INFINITY;
     if (lane < p.k) {
@@ -619,41 +929,49 @@ __global__ void __launch_bounds__(256) moe_topk_grad_kernel(const __grid_constan
       g = p.scale * p.grad_weights[t * p.k + lane];
       lv = load_logit<BF16>(p.logits, t * p.E + pick);
     }
+    float l[VPL];
+    load_row<BF16, VPL>(p.logits, t, p.E, lane, l);
+    if (p.grad_scores != nullptr) load_bias<VPL>(p.grad_scores + t * p.E, p.E, lane, d);
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) chosen[lane * VPL + j] = 0.0f;
+    __syncwarp();
     if (p.renorm) {
-      const float share = share_of(p.score, lv, pick >= 0);
+      const float share = share_of(p.score, lv, 32);
       const float mean = warp_add(pick >= 0 ? g * share : 0.0f);
       g = share * (g - mean);  // to the logit itself
       // 1 - s without the cancellation
       if (p.score == MOE_SCORE_SIGMOID) g = pick >= 0 ? g / (1.0f + expf(lv)) : 0.0f;
     }
-    float direct[VPL];
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int e = lane * VPL + j;
-      direct[j] = 0.0f;
-      d[j] = p.grad_scores != nullptr && e < p.E ? p.grad_scores[t * p.E + e] : 0.0f;
+    const unsigned same = __match_any_sync(kFull, pick);
+    if (__all_sync(kFull, pick < 0 || (same & (same - 1)) == 0)) {
+      if (pick >= 0) chosen[pick] = g;
+      __syncwarp();
+    } else {
+      for (int i = 0; i < p.k; ++i) {
+        if (lane == i && pick >= 0) chosen[pick] += g;
+        __syncwarp();
+      }
     }
-    for (int i = 0; i < p.k; ++i) {
-      const int e = __shfl_sync(kFull, pick, i);
-      const float v = __shfl_sync(kFull, g, i);
-      const int j0 = e - lane * VPL;  // outside [0, VPL): another lane's, or none
-#pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (e >= 0 && j == j0) {
-          if (p.renorm) direct[j] += v;
-          else d[j] += v;
-        }
-    }
+    // renormalised weights reach the logits directly, the others through the scores
     if (p.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) d[j] = d[j] * s[j] / (1.0f + expf(l[j])) + direct[j];
+      for (int j = 0; j < VPL; ++j) {
+        const float c = chosen[lane * VPL + j];
+        // s (1 - s) = e / (1 + e)^2 with e = exp(-|l|)
+        const float e = ex2_fast(-kLog2e * fabsf(l[j])), r = rcp_fast(1.0f + e);
+        d[j] = p.renorm ? fmaf(d[j], e * r * r, c) : (d[j] + c) * (e * r * r);
+      }
     } else {
-      float dot = 0.0f;
+      float s[VPL], z, top, dot = 0.0f;
+      row_scores<VPL>(p.score, l, s, top, z);
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) dot += s[j] > 0.0f ? d[j] * s[j] : 0.0f;
+      for (int j = 0; j < VPL; ++j) {
+        if (!p.renorm) d[j] += chosen[lane * VPL + j];
+        dot += s[j] > 0.0f ? d[j] * s[j] : 0.0f;
+      }
       dot = warp_add(dot);
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) d[j] = s[j] * (d[j] - dot) + direct[j];
+      for (int j = 0; j < VPL; ++j) d[j] = fmaf(s[j], d[j] - dot, p.renorm ? chosen[lane * VPL + j] : 0.0f);
     }
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
@@ -715,7 +1033,7 @@ TopkLayout plan_topk(int64_t T, int32_t E) {
   L.status = 0;
   L.hist = 256;
   L.totals = L.hist + up(sizeof(int32_t) * L.nblk * E);
-  L.total = L.nblk > 1 ? L.totals + up(sizeof(int32_t) * E) : 0;
+  L.total = L.nblk > kClusterBlocks ? L.totals + up(sizeof(int32_t) * E) : 0;
   return L;
 }
 
@@ -772,7 +1090,7 @@ moe_status_t moe_topk_route(const moe_topk_args_t* a, const moe_topk_routed_t* r
       !aligned16(r->scores) || (reinterpret_cast<uintptr_t>(a->n_tokens) & 3u) != 0)
     return MOE_ERR_MISALIGNED;
   const TopkLayout L = plan_topk(a->T, a->E);
-  const bool ws = dispatch && L.nblk > 1;
+  const bool ws = dispatch && L.nblk > kClusterBlocks;
   if (ws && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < L.total))
     return MOE_ERR_WORKSPACE;
   TopkParams p{};
@@ -805,17 +1123,35 @@ moe_status_t moe_topk_route(const moe_topk_args_t* a, const moe_topk_routed_t* r
     p.status = static_cast<uint32_t*>(workspace);
   }
   const unsigned grid = static_cast<unsigned>(L.nblk);
+  const bool few = L.nblk <= device_sm_count();
+  const bool cluster = dispatch && L.nblk > 1 && L.nblk <= kClusterBlocks;
   const cudaError_t e = with_vpl(a->E, [&](auto v) {
     constexpr int VPL = decltype(v)::value;
-    if (a->dtype == MOE_BF16) moe_topk_route_kernel<true, VPL><<<grid, kTopkWarps * 32, 0, s>>>(p);
-    else moe_topk_route_kernel<false, VPL><<<grid, kTopkWarps * 32, 0, s>>>(p);
-    return cudaGetLastError();
+    constexpr int WIDE = VPL <= 8 ? 32 : 16;
+    const int run = p.group_size / VPL;
+    p.lane_run = p.group_size % VPL == 0 && (run & (run - 1)) == 0 ? run : 0;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster ? grid : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(few ? WIDE * 32 : 8 * 32, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 1 : 0;
+    if (a->dtype == MOE_BF16)
+      return few ? cudaLaunchKernelEx(&cfg, moe_topk_route_kernel<true, VPL, WIDE>, p)
+                 : cudaLaunchKernelEx(&cfg, moe_topk_route_kernel<true, VPL, 8>, p);
+    return few ? cudaLaunchKernelEx(&cfg, moe_topk_route_kernel<false, VPL, WIDE>, p)
+               : cudaLaunchKernelEx(&cfg, moe_topk_route_kernel<false, VPL, 8>, p);
   });
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   if (ws) {
     moe_topk_scan_kernel<<<(a->E + 31) / 32, 1024, 0, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-    moe_topk_dispatch_kernel<<<grid, kTopkWarps * 32, 0, s>>>(p);
+    moe_topk_dispatch_kernel<<<grid, kDispatchWarps * 32, 0, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;
@@ -832,11 +1168,11 @@ moe_status_t moe_topk_route_backward(const moe_topk_args_t* a, const int32_t* id
   TopkGradParams p{a->logits, a->n_tokens, idx, grad_weights, grad_scores, grad_logits, a->T, a->E,
                    a->k,      a->score,    a->renormalize, a->scale};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>((a->T + 7) / 8);
+  const unsigned grid = static_cast<unsigned>((a->T + kGradWarps - 1) / kGradWarps);
   const cudaError_t e = with_vpl(a->E, [&](auto v) {
     constexpr int VPL = decltype(v)::value;
-    if (a->dtype == MOE_BF16) moe_topk_grad_kernel<true, VPL><<<grid, 256, 0, s>>>(p);
-    else moe_topk_grad_kernel<false, VPL><<<grid, 256, 0, s>>>(p);
+    if (a->dtype == MOE_BF16) moe_topk_grad_kernel<true, VPL><<<grid, kGradWarps * 32, 0, s>>>(p);
+    else moe_topk_grad_kernel<false, VPL><<<grid, kGradWarps * 32, 0, s>>>(p);
     return cudaGetLastError();
   });
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

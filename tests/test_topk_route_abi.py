@@ -19,7 +19,7 @@ def built_library():
     return N.lib()
 
 
-def args(T=64, E=16, k=2, dtype=N.MOE_F32, score=0, n_groups=1, topk_groups=1, rule=0, renorm=0, scale=1.0,
+def args(T=400, E=16, k=2, dtype=N.MOE_F32, score=0, n_groups=1, topk_groups=1, rule=0, renorm=0, scale=1.0,
          logits=BASE, bias=None, n_tokens=None):
     return N.MoeTopkArgs(logits, bias, n_tokens, T, E, k, dtype, score, n_groups, topk_groups, rule, renorm, scale)
 
@@ -71,8 +71,8 @@ def test_route_refuses_outputs_and_workspace():
 def test_workspace_size():
     size = moe.moe_topk_workspace_size
     assert size(0, 8, 2) == size(-1, 8, 2) == size(64, 2000, 2) == size(64, 8, 9) == 0
-    assert size(32, 256, 8) == 0                      # one block: nothing kept between kernels
-    assert size(33, 256, 8) >= 2 * 256 * 4 and size(33, 256, 8) % 256 == 0
+    assert size(256, 256, 8) == 0                     # one launch: nothing kept between kernels
+    assert size(257, 256, 8) >= 9 * 256 * 4 and size(257, 256, 8) % 256 == 0
     assert size(1 << 24, 1024, 8) > (1 << 24) // 32 * 1024 * 4   # past 32 bits
 
 

@@ -163,21 +163,21 @@ def test_route_padded_batch(T, n):
 
 
 def test_route_without_dispatch_and_with_given_outputs():
-    l = logits_of(200, 64, torch.float32, 6)
+    l = logits_of(300, 64, torch.float32, 6)
     full = run_and_check(l, 4, "softmax")
     bare = moe.moe_topk_route(l, 4, dispatch=False)
     assert set(bare) == {"idx", "weights"}
     assert torch.equal(bare["idx"], full["idx"]) and torch.equal(bare["weights"], full["weights"])
     out = {n: torch.full_like(t, 77) for n, t in full.items()}
-    ws = torch.full((moe.moe_topk_workspace_size(200, 64, 4),), 255, dtype=torch.uint8, device=DEV)
+    ws = torch.full((moe.moe_topk_workspace_size(300, 64, 4),), 255, dtype=torch.uint8, device=DEV)
     got = moe.moe_topk_route(l, 4, out=out, workspace=ws)
     for name in out:
         assert got[name] is out[name] and torch.equal(got[name], full[name])
     assert moe.moe_device_status(ws) == (0, 0)
     with pytest.raises(ValueError):
-        moe.moe_topk_route(l, 4, out={"scores": torch.empty(200, 64, device=DEV)})
+        moe.moe_topk_route(l, 4, out={"scores": torch.empty(300, 64, device=DEV)})
     with pytest.raises(ValueError):
-        moe.moe_topk_route(l, 4, out={"idx": torch.empty(200, 5, dtype=torch.int32, device=DEV)})
+        moe.moe_topk_route(l, 4, out={"idx": torch.empty(300, 5, dtype=torch.int32, device=DEV)})
     with pytest.raises(ValueError):
         moe.moe_topk_route(l.t(), 4)
     with pytest.raises(moe.MoeError):
