@@ -15,10 +15,9 @@ Tensors, devices, streams and errors as in the routing calls.
 
 from __future__ import annotations
 
-import ctypes
-
 from . import _native as N
-from .routed import _check, _codes, _need, _place, _refuse
+from . import routed as _r
+from .routed import _check, _code, _first, _need, _on, _refuse
 
 __all__ = ["moe_int8_product", "moe_int8_workspace_size"]
 
@@ -40,36 +39,46 @@ def moe_int8_product(x, w, s, *, x_scale=None, index=None, counts=None, w_up=Non
     as they were (an output that is not given starts as zeros then). ``out_dtype``: bf16
     (the default) or fp32. ``workspace``: uint8 tensor of moe_int8_workspace_size bytes;
     moe_device_status reads its status word."""
-    import torch
-
-    if x.dim() != 2 or w.dim() != 3:
-        _refuse("x must be [rows, K] and w [n_experts, K, N]")
-    n, K, cols = w.shape
-    dev = x.device
-    i8, b16 = torch.int8, torch.bfloat16
-    x_code = N.MOE_INT8 if x.dtype == i8 else _codes().get(x.dtype)
-    if x_code is None:
-        _refuse(f"x has type {x.dtype}, not bf16, fp32 or int8")
-    R = x.shape[0] if index is None else index.shape[0]
+    dev = _first(x, "x", 2)
+    _first(w, "w", 3)
+    f32, i32, i8, b16 = _r._F32, _r._I32, _r._I8, _r._BF16
+    rows, xt = x.shape[0], x.dtype
+    n, K, cols = shape = w.shape
+    x_code = N.MOE_INT8 if xt is i8 else _code(xt, "x")
+    if x.shape[1] != K:
+        _refuse(f"x has rows of {x.shape[1]}, w of {K}")
+    R = rows if index is None else index.shape[0]
     if (w_up is None) != (s_up is None):
         _refuse("w_up and s_up come together")
-    a = N.MoeInt8Args(
-        _need(x, "x", (x.shape[0], K), (x.dtype,), None), _need(x_scale, "x_scale", (R,), (torch.float32,), dev),
-        _need(index, "index", (R,), (torch.int32,), dev), _need(counts, "counts", (n,), (torch.int32,), dev),
-        _need(w, "w", (n, K, cols), (i8,), dev), _need(w_up, "w_up", (n, K, cols), (i8,), dev),
-        _need(s, "s", (n, cols), (b16,), dev), _need(s_up, "s_up", (n, cols), (b16,), dev),
-        _need(gate, "gate", (R,), (torch.float32,), dev), None, x.shape[0], R, K, cols, n, x_code, N.MOE_BF16, activation)
-    with _place(dev, stream) as handle:
-        if out is None:
-            out = (torch.empty if counts is None else torch.zeros)((R, cols), dtype=out_dtype or b16, device=dev)
-        elif out_dtype is not None and out.dtype != out_dtype:
-            _refuse(f"out has type {out.dtype}, not {out_dtype}")
-        a.out = _need(out, "out", (R, cols), (b16, torch.float32), dev)
-        a.out_dtype = _codes()[out.dtype]
+    xp = x.data_ptr()
+    ptrs = (_need(x_scale, "x_scale", (R,), f32, dev), _need(index, "index", (R,), i32, dev),
+            _need(counts, "counts", (n,), i32, dev), _need(w, "w", shape, i8, dev),
+            _need(w_up, "w_up", shape, i8, dev), _need(s, "s", (n, cols), b16, dev),
+            _need(s_up, "s_up", (n, cols), b16, dev), _need(gate, "gate", (R,), f32, dev))
+
+    def call(handle):
+        o = out
+        if o is None:
+            import torch
+
+            o = (torch.empty if counts is None else torch.zeros)((R, cols), dtype=out_dtype or b16, device=dev)
+        elif out_dtype is not None and o.dtype is not out_dtype:
+            _refuse(f"out has type {o.dtype}, not {out_dtype}")
+        dtype = o.dtype
+        out_code = _code(dtype, "out")
+        a = N.MoeInt8Args(xp, *ptrs, _need(o, "out", (R, cols), dtype, dev), rows, R, K, cols, n, x_code, out_code,
+                          activation)
+        L = N.lib()
         if workspace is None:
-            size = N.lib().moe_int8_workspace_size(R, K, cols, n, x_code, int(w_up is not None))
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-        st = N.lib().moe_int8_product(ctypes.byref(a), _need(workspace, "workspace", workspace.shape, (torch.uint8,), dev),
-                                      workspace.numel(), handle)
-    _check(st, "moe_int8_product")
-    return out
+            from torch import empty
+
+            size = L.moe_int8_workspace_size(R, K, cols, n, x_code, 0 if w_up is None else 1)
+            held = empty(size, dtype=_r._U8, device=dev)
+            ws = held.data_ptr()
+        else:
+            size = workspace.numel()
+            ws = _need(workspace, "workspace", (size,), _r._U8, dev)
+        _check(L.moe_int8_product(a, ws, size, handle), "moe_int8_product")
+        return o
+
+    return _on(dev, stream, call)
