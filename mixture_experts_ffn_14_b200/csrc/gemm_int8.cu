@@ -37,9 +37,8 @@ constexpr int kMaxCtas = 160;        // product CTAs at most (workspace sizing; 
 
 // Tile schedule in the workspace, made by the prepare kernel.
 struct Sched {
-  int32_t cnt[kMaxExperts];      // rows of each expert
-  int32_t off[kMaxExperts];      // first row
-  int32_t pre[kMaxExperts + 1];  // row tiles before each expert
+  int32_t off[kMaxExperts + 1];  // first row of each expert, and the end of the last one
+  int32_t pre[kMaxExperts + 1];  // row tiles before each expert, and all of them
 };
 
 // ---------------------------------------------------------------- prepare --
@@ -124,11 +123,9 @@ __device__ void make_schedule(const PrepParams& p) {
     const long long left = at < p.R ? p.R - at : 0;
     const int cut = static_cast<int>(c[j] < left ? c[j] : left);
     if (cut < c[j]) bad = true;
-    if (e < p.n_experts) {
-      p.sched->cnt[e] = cut;
-      p.sched->off[e] = static_cast<int32_t>(at < p.R ? at : p.R);
-    }
+    if (e < p.n_experts) p.sched->off[e] = static_cast<int32_t>(at < p.R ? at : p.R);
     at += c[j];
+    if (e == p.n_experts - 1) p.sched->off[p.n_experts] = static_cast<int32_t>(at < p.R ? at : p.R);
     mine[j] = (cut + p.tile_rows - 1) / p.tile_rows;
     tiles += mine[j];
   }
@@ -187,13 +184,19 @@ __device__ __forceinline__ void unpack(const Raw<BF16>& r, float (&f)[8]) {
   }
 }
 
-// A quotient this close to a half (of the fp32 product x * (127 / top), which is off by
-// at most 127 * 2^-24 < 8e-6, the reciprocal's rounding) is decided exactly.
-constexpr float kNearHalf = 0.5f - 1e-5f;
+// ---- exact quotients --------------------------------------------------------
+// q = 127 x / top rounded to nearest, ties to even, as the exact quotient rounds. With
+// y0 = a / top approximately, a = 127 x, the residual a - y0 top is exact in fp32 for a
+// bf16 row (15 + 8 bits), and y = y0 + residual / top is the quotient within an ulp, and
+// exactly the quotient where that has few bits, as every half has. A bf16 quotient
+// that is no half is at least 2^-16 of itself away from one (254 m_x and (2 n + 1) m_a are
+// integers, m_x < 256), so rounding y decides. Ties are common there (about one value
+// in a hundred), so they must cost nothing: sending them to a careful path doubled
+// the kernel's time. An fp32 quotient can lie as near as 2^-33 to a half: those within two
+// ulp are compared exactly.
 
-// 127 x / top rounded to nearest, ties to even, as the exact quotient rounds; `low` is
-// the integer below it. Compares 254 x with (2 low + 1) top: both products in two
-// parts (value and exact remainder; 32 bits each, so the parts' differences are exact).
+// 254 x against (2 low + 1) top, low the integer below: both products in two parts (value
+// and exact remainder; 32 bits each, so the parts' differences are exact).
 __device__ __forceinline__ int quantise_near_half(float x, float top, float low) {
   const float odd = 2.0f * low + 1.0f;
   const float a = 254.0f * x, b = odd * top;
@@ -202,52 +205,47 @@ __device__ __forceinline__ int quantise_near_half(float x, float top, float low)
   return d > 0.0f ? l + 1 : (d < 0.0f ? l : l + (l & 1));
 }
 
-// The vectors that hold such a quotient, and those of rows next to the ends of the fp32
-// range (scale != 1).
-template <bool BF16>
-__device__ __noinline__ uint2 quantise8_near(Raw<BF16> r, float rcp, float scale, float top) {
-  float f[8];
-  unpack<BF16>(r, f);
-  uint32_t q[2] = {0, 0};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float x = f[j] * scale, y = x * rcp, m = rintf(y);
-    int n = static_cast<int>(m);
-    if (fabsf(y - m) > kNearHalf) n = quantise_near_half(x, top, y < m ? m - 1.0f : m);
-    q[j / 4] |= static_cast<uint32_t>(n & 0xff) << (8 * (j % 4));
-  }
-  return make_uint2(q[0], q[1]);
-}
-
 // What the quotients of a row need, from the bits of its largest magnitude.
 struct RowScale {
-  float rcp, scale, top;
+  float inv, scale, top;
   bool zero;  // q = 0; a = NaN or 0
   bool far;   // next to an end of the fp32 range: every vector takes the careful path
 
   __device__ __forceinline__ explicit RowScale(uint32_t top_bits) {
     const float t = __uint_as_float(top_bits);
     zero = top_bits >= 0x7f800000u || top_bits == 0;
-    // Such rows are moved by a power of two (exact for every value that is not far
-    // below the largest), so that no product leaves the range.
+    // moved by a power of two (exact for every value that is not far below the
+    // largest), so that no product leaves the range
     scale = t < 1e-30f ? 0x1p80f : (t > 1e30f ? 0x1p-30f : 1.0f);
     far = scale != 1.0f;
     top = t * scale;
-    rcp = 127.0f / top;
+    inv = 1.0f / top;
   }
 };
 
-__device__ __forceinline__ float row_step(uint32_t top_bits) {
-  return top_bits < 0x7f800000u ? __uint_as_float(top_bits) / 127.0f : __uint_as_float(0x7fc00000u);
+constexpr float kNearHalf = 0.5f - 2e-5f;  // two ulp of 127
+
+template <bool BF16>
+__device__ __noinline__ uint2 quantise8_near(Raw<BF16> r, float inv, float scale, float top) {
+  float f[8];
+  unpack<BF16>(r, f);
+  uint32_t q[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = f[j] * scale, y = 127.0f * x * inv, m = rintf(y);
+    int n = static_cast<int>(m);
+    if (fabsf(y - m) > 0.4999f) n = quantise_near_half(x, top, y < m ? m - 1.0f : m);
+    q[j / 4] |= static_cast<uint32_t>(n & 0xff) << (8 * (j % 4));
+  }
+  return make_uint2(q[0], q[1]);
 }
 
-// Eight quotients to bytes. Adding 1.5 * 2^23 to a product leaves it rounded to an
-// integer (ties to even) in the low mantissa bits; a vector with a quotient next to a
-// half (one in six thousand) is looked at again. A warp that does holds up its row's
-// group at the next barrier, so these must be few.
+// Eight quotients to bytes. Adding 1.5 * 2^23 leaves a quotient rounded to an integer
+// (ties to even) in the low mantissa bits.
 template <bool BF16>
 __device__ __forceinline__ uint2 quantise8(Raw<BF16> r, const RowScale& s) {
   if (s.zero) return make_uint2(0, 0);
+  if (s.far) return quantise8_near<BF16>(r, s.inv, s.scale, s.top);
   constexpr float kMagic = 12582912.0f;
   float f[8];
   unpack<BF16>(r, f);
@@ -255,11 +253,13 @@ __device__ __forceinline__ uint2 quantise8(Raw<BF16> r, const RowScale& s) {
   float off = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float m = fmaf(f[j], s.rcp, kMagic);
+    const float a = 127.0f * f[j], y0 = a * s.inv;
+    const float y = fmaf(fmaf(-y0, s.top, a), s.inv, y0);
+    const float m = y + kMagic;
     t[j] = __float_as_uint(m);
-    off = fmaxf(off, fabsf(fmaf(f[j], s.rcp, kMagic - m)));
+    if (!BF16) off = fmaxf(off, fabsf(y - (m - kMagic)));
   }
-  if (off > kNearHalf || s.far) return quantise8_near<BF16>(r, s.rcp, s.scale, s.top);
+  if (!BF16 && off > kNearHalf) return quantise8_near<BF16>(r, s.inv, s.scale, s.top);
   return make_uint2(
       __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
       __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
@@ -287,15 +287,20 @@ __device__ __forceinline__ uint32_t largest_bits(uint32_t top) {
   return BF16 ? max(top << 16, top & 0xffff0000u) : top;
 }
 
+// The row's scale: the largest magnitude over 127, the correctly rounded quotient.
+__device__ __forceinline__ float row_step(uint32_t top_bits) {
+  return top_bits < 0x7f800000u ? __uint_as_float(top_bits) / 127.0f : __uint_as_float(0x7fc00000u);
+}
+
 // Rows to 8 bits, bound by memory: groups of NT threads take rows in turn; up to kRing
 // rows of each group are on their way into shared memory as bulk copies while one is worked
 // on, and a row goes from there to registers once (its largest magnitude as bits, so
 // that NaN and infinity win; then the quotients). One barrier per row. The schedule is
 // made by the last CTA, which has the fewest rows.
-constexpr int kPrepCta = 1024;
+constexpr int kPrepCta = 512;
 constexpr int kRing = 4;
 constexpr int kRingBytes = 200 * 1024;  // shared memory for rows on their way
-constexpr int kPrepVec = 4;             // vectors of 8 values per thread
+constexpr int kPrepVec = 8;             // vectors of 8 values per thread: few warps per row, as each has its own overhead
 
 template <bool BF16, int NT>
 __global__ void __launch_bounds__(kPrepCta, 1)
@@ -382,7 +387,7 @@ __global__ void __launch_bounds__(kPrepCta, 1)
 // (the second time from L2).
 template <bool BF16>
 __global__ void __launch_bounds__(kPrepCta) moe_int8_prepare_long_kernel(const __grid_constant__ PrepParams p) {
-  __shared__ uint32_t part[32];
+  __shared__ uint32_t part[kPrepCta / 32];
   if (blockIdx.x == 0) {
     if (threadIdx.x < kPrepThreads) make_schedule(p);
     return;
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(kPrepCta) moe_int8_prepare_long_kernel(const _
   top_bits = __reduce_max_sync(0xffffffffu, largest_bits<BF16>(top_bits));
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top_bits;
   __syncthreads();
-  top_bits = __reduce_max_sync(0xffffffffu, part[threadIdx.x % 32]);
+  top_bits = __reduce_max_sync(0xffffffffu, part[threadIdx.x % (kPrepCta / 32)]);
   const RowScale rs(top_bits);
   if (threadIdx.x == 0) p.a[r] = row_step(top_bits);
   uint2* dst = reinterpret_cast<uint2*>(p.q + r * p.K);
@@ -423,17 +428,36 @@ struct Params {
   int32_t group_rows, group_limit;  // pair form: row tiles per L2 group (tile_order.cuh)
 };
 
-// Gate activation in fp32: z * sigmoid(.) forms, which keep the relative accuracy
-// of large negative z (1 + tanh would cancel); the approximate exponential and
-// quotient are off by about 2^-21, below the rounding of either output type's sums.
-__device__ __forceinline__ float act_f32(float z, int mode) {
-  if (mode == MOE_ACT_GELU_ERF) return 0.5f * z * erfcf(-0.70710678118654752f * z);
-  const float t = mode == MOE_ACT_SILU ? z : 1.5957691216057308f * (z + 0.044715f * z * z * z);
-  return __fdividef(z, 1.0f + __expf(-t));
+// 2^x within 2 ulp and 1 / x within 1 ulp, results below the normal range as zero.
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// Gate activations of N values in fp32, as z * sigmoid(t): that keeps the relative
+// accuracy of large negative z (1 + tanh would cancel), and is two special-function
+// instructions. The mode is looked at once for all of them.
+//   GELU (tanh form) = z / (1 + e^-t), t = 2 sqrt(2 / pi) (z + 0.044715 z^3); SiLU: t = z
+template <int N>
+__device__ __forceinline__ void activate(float (&z)[N], int mode) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  constexpr float kTanh = 1.5957691216057308f;
+  if (mode == MOE_ACT_GELU_ERF) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) z[j] *= 0.5f * erfcf(-0.70710678118654752f * z[j]);
+  } else {
+    const float c1 = mode == MOE_ACT_SILU ? -kLog2e : -kLog2e * kTanh;
+    const float c3 = mode == MOE_ACT_SILU ? 0.0f : -kLog2e * kTanh * 0.044715f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) z[j] *= rcp_fast(1.0f + ex2_fast(z[j] * fmaf(z[j] * z[j], c3, c1)));
+  }
+}
 
 // Index of the expert that holds row tile `m` (pre[e] <= m < pre[e + 1]).
 __device__ __forceinline__ int expert_of(const int32_t* pre, int n, int m) {
@@ -489,6 +513,7 @@ __global__ void __launch_bounds__(256, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* last_flag = abort_flag + 1;
   int32_t* pre = reinterpret_cast<int32_t*>(full_bar) + 64;  // 256 B after the barriers' start
+  int32_t* off = pre + p.n_experts + 1;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
@@ -511,7 +536,10 @@ __global__ void __launch_bounds__(256, 1)
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
-  for (int e = threadIdx.x; e <= p.n_experts; e += 256) pre[e] = p.sched->pre[e];
+  for (int e = threadIdx.x; e <= p.n_experts; e += 256) {
+    pre[e] = p.sched->pre[e];
+    off[e] = p.sched->off[e];
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -553,9 +581,8 @@ __global__ void __launch_bounds__(256, 1)
     const int local = static_cast<int>(tile - static_cast<int64_t>(pre[s.e]) * p.nt);
     const int m = local % mt;  // row tiles run fastest: those that share weights follow one another
     s.n0 = (local / mt) * (DUAL ? 128 : 256);
-    const int cnt = p.sched->cnt[s.e];
-    s.row0 = p.sched->off[s.e] + m * ROWS;
-    s.rows = min(ROWS, cnt - m * ROWS);
+    s.row0 = off[s.e] + m * ROWS;
+    s.rows = min(ROWS, off[s.e + 1] - s.row0);
     return true;
   };
 
@@ -658,6 +685,23 @@ __global__ void __launch_bounds__(256, 1)
     Seg s;
     Cursor cur{lo, 0};
     while (next(cur, s)) {
+      // What the finished tile needs besides its sums, on its way before they are: this
+      // lane's channel scales, and the scale (with the gate) of rows lane, lane + 32, ...
+      const int ca = s.n0 + col, cb = DUAL ? ca : ca + 128;
+      const bool va = ca < p.N, vb = cb < p.N;
+      const int64_t se = static_cast<int64_t>(s.e) * p.N;
+      const float sa = va ? __bfloat162float(p.s0[se + ca]) : 0.0f;
+      const float sb = vb ? __bfloat162float((DUAL ? p.s1 : p.s0)[se + cb]) : 0.0f;
+      float ra[ROWS / 32], rg[ROWS / 32];
+#pragma unroll
+      for (int i = 0; i < ROWS / 32; ++i) {
+        const int64_t row = s.row0 + 32 * i + lane;
+        const bool in = 32 * i + lane < s.rows;
+        // the row's scale, and with the gate: of the up product, or of the only one
+        ra[i] = in ? __ldg(p.a + row) : 0.0f;
+        rg[i] = in && p.gate != nullptr ? ra[i] * __ldg(p.gate + row) : ra[i];
+        if (!DUAL) ra[i] = rg[i];
+      }
       if (!warp_wait(&tfull_bar[acc], acc_phase, abort_flag)) {
         atomicOr(p.status, kStatusEpilogueTimeout);
         *abort_flag = 1;
@@ -696,16 +740,13 @@ __global__ void __launch_bounds__(256, 1)
         if (finish) __threadfence();
       }
       if (finish) {
-        const int ca = s.n0 + col, cb = DUAL ? ca : ca + 128;
-        const bool va = ca < p.N, vb = cb < p.N;
-        const int64_t se = static_cast<int64_t>(s.e) * p.N;
-        const float sa = va ? __bfloat162float(p.s0[se + ca]) : 0.0f;
-        const float sb = vb ? __bfloat162float((DUAL ? p.s1 : p.s0)[se + cb]) : 0.0f;
-#pragma unroll 1
-        for (int j0 = 0; j0 < s.rows; j0 += 16) {
+#pragma unroll
+        for (int j0 = 0; j0 < ROWS; j0 += 16) {
+          if (j0 >= s.rows) break;
           uint32_t u[16], v[16];
           tmem_ld16x2(tb + j0, tb + ROWS + j0, u, v);
           if (!whole) {
+#pragma unroll 1
             for (int c = first; c <= last; ++c) {
               if (c == me) continue;
               const int32_t* o = p.part + (2 * static_cast<int64_t>(c) + (c == first ? 1 : 0)) * C::PART_INTS;
@@ -717,24 +758,31 @@ __global__ void __launch_bounds__(256, 1)
                 }
             }
           }
+          float za[16], zb[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            if (j0 + j >= s.rows) continue;
-            const int64_t row = s.row0 + j0 + j;
-            const float a = __ldg(p.a + row), g = p.gate != nullptr ? __ldg(p.gate + row) : 1.0f;
-            const float za = static_cast<float>(static_cast<int>(u[j])) * a * sa;
-            const float zb = static_cast<float>(static_cast<int>(v[j])) * a * sb;
-            auto put = [&](int c, float y) {
-              if (OB) static_cast<__nv_bfloat16*>(p.out)[row * p.N + c] = __float2bfloat16_rn(y);
-              else static_cast<float*>(p.out)[row * p.N + c] = y;
-            };
-            if (DUAL) {
-              if (va) put(ca, act_f32(za, p.act) * zb * g);
-            } else {
-              if (va) put(ca, za * g);
-              if (vb) put(cb, zb * g);
-            }
+            const float a = __shfl_sync(0xffffffffu, ra[j0 / 32], j0 % 32 + j);
+            const float b = DUAL ? __shfl_sync(0xffffffffu, rg[j0 / 32], j0 % 32 + j) : a;
+            za[j] = static_cast<float>(static_cast<int>(u[j])) * sa * a;
+            zb[j] = static_cast<float>(static_cast<int>(v[j])) * sb * b;
           }
+          if (DUAL) {
+            activate(za, p.act);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) za[j] *= zb[j];
+          }
+          auto put = [&](auto* out) {
+            using T = std::remove_pointer_t<decltype(out)>;
+            T* o = out + (static_cast<int64_t>(s.row0) + j0) * p.N;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (j0 + j >= s.rows) break;
+              if (va) o[static_cast<int64_t>(j) * p.N + ca] = static_cast<T>(za[j]);
+              if (!DUAL && vb) o[static_cast<int64_t>(j) * p.N + cb] = static_cast<T>(zb[j]);
+            }
+          };
+          if (OB) put(static_cast<__nv_bfloat16*>(p.out));
+          else put(static_cast<float*>(p.out));
         }
       }
       if (!whole) asm volatile("bar.sync 1, 128;" ::: "memory");  // last_flag read by all before the next one
@@ -769,8 +817,13 @@ constexpr int PX_BYTES = 128 * BK;              // 16 KB: this CTA's 128 rows
 constexpr int PSTAGE_BYTES = PX_BYTES + WBOX;   // 32 KB
 constexpr int PSTAGES = 6;
 constexpr int PQ = 4;             // tile-id queue: the producer leads by at most 3 tiles
-constexpr int PQ_READERS = 10;    // odd producer, MMA thread, 4 epilogue warps x 2 CTAs
-constexpr int PSMEM = PSTAGES * PSTAGE_BYTES + 1024 + 256 + (kMaxExperts + 1) * 4;
+// Epilogue warps: sets of four (one per 32 TMEM lanes), each set with its own columns.
+constexpr int PSETS = 4;
+constexpr int PEPI = 4 * PSETS;
+constexpr int PTHREADS = 128 + 32 * PEPI;
+constexpr int PQ_READERS = 2 + 2 * PEPI;  // odd producer, MMA thread, the epilogue warps of both CTAs
+constexpr int PSCALES = 2 * 128 / PSETS;  // channel scales an epilogue warp keeps in shared memory
+constexpr int PSMEM = PSTAGES * PSTAGE_BYTES + 1024 + 256 + PEPI * PSCALES * 4 + 2 * (kMaxExperts + 1) * 4;
 static_assert(PSMEM <= 232448, "shared memory above the per-block limit");
 static_assert((2 * PSTAGES + 4 + 2 * PQ + 1) * 8 + 8 + 4 * PQ <= 256, "barrier area too small");
 
@@ -797,69 +850,72 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 
-// One row (thread) of an epilogue warp: 16-column steps of the accumulator, scaled,
-// activated and stored as 32 or 64 contiguous bytes.
-template <bool DUAL, bool OB>
-__device__ __forceinline__ void pair_epilogue(const Params& p, int e, int n0, uint32_t tb, int64_t row, bool valid) {
+// Columns of one epilogue warp: accumulator columns [c0, c0 + PCOLS) of a plain product
+// (its scales in sc[0 .. PCOLS)), or PCOLS / 2 gate columns from c0 and the up columns
+// 128 further on (scales of both halves).
+constexpr int PCOLS = 256 / PSETS;
+
+template <bool DUAL>
+__device__ __forceinline__ void pair_scales(const Params& p, int e, int n0, int c0, int lane, float* sc) {
   const int64_t se = static_cast<int64_t>(e) * p.N;
-  const float a = valid ? __ldg(p.a + row) : 0.0f;
-  const float g = valid && p.gate != nullptr ? __ldg(p.gate + row) : 1.0f;
-  auto scales = [&](const __nv_bfloat16* s, int c, float (&f)[16]) {
-    const uint4* q = reinterpret_cast<const uint4*>(s + se + c);
-    const uint4 u = __ldg(q), v = __ldg(q + 1);
-    const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      f[2 * j] = bf16_lo(w[j]);
-      f[2 * j + 1] = bf16_hi(w[j]);
-    }
-  };
+  for (int i = 0; i < PCOLS / 32; ++i) {
+    const int j = 32 * i + lane;
+    const bool up = DUAL && j >= PCOLS / 2;
+    const int c = n0 + c0 + (up ? j - PCOLS / 2 : j);
+    sc[j] = c < p.N ? __bfloat162float((up ? p.s1 : p.s0)[se + c]) : 0.0f;
+  }
+  __syncwarp();
+}
+
+// One row (thread) of a tile, its sums in registers (u, v: the gate and up columns, or
+// 32 columns and the next 32): scaled, activated and stored as 32 or 64 contiguous
+// bytes at a time. a, ag: the row's scale, and that times its gate.
+template <bool DUAL, bool OB>
+__device__ __forceinline__ void pair_epilogue(const Params& p, int n0, const uint32_t (&u)[32], const uint32_t (&v)[32],
+                                              const float* sc, int64_t row, float a, float ag) {
+  static_assert(PCOLS == 64, "two registers sets of 32 columns");
   auto put16 = [&](int c, const float (&y)[16]) {
-    if (!valid) return;
+    if (n0 + c >= p.N) return;  // N is a multiple of 16
     if (OB) {
-      uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * p.N + c);
+      uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * p.N + n0 + c);
 #pragma unroll
-      for (int v = 0; v < 2; ++v)
-        d[v] = make_uint4(pack_bf16x2(y[8 * v], y[8 * v + 1]), pack_bf16x2(y[8 * v + 2], y[8 * v + 3]),
-                          pack_bf16x2(y[8 * v + 4], y[8 * v + 5]), pack_bf16x2(y[8 * v + 6], y[8 * v + 7]));
+      for (int i = 0; i < 2; ++i)
+        d[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                          pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
     } else {
-      float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.N + c);
+      float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.N + n0 + c);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) d[v] = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
+      for (int i = 0; i < 4; ++i) d[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
     }
   };
-#pragma unroll 1
-  for (int c = 0; c < (DUAL ? 128 : 256); c += DUAL ? 16 : 32) {
-    if (n0 + c >= p.N) break;  // N is a multiple of 16
-    const bool second = DUAL || n0 + c + 16 < p.N;
-    float s0[16], s1[16], y[16];
-    scales(p.s0, n0 + c, s0);
-    if (second) scales(DUAL ? p.s1 : p.s0, DUAL ? n0 + c : n0 + c + 16, s1);
-    uint32_t u[16], v[16];
-    tmem_ld16x2(tb + c, tb + c + (DUAL ? 128 : 16), u, v);
-    if (DUAL) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float z = static_cast<float>(static_cast<int>(u[j])) * a * s0[j];
-        const float z1 = static_cast<float>(static_cast<int>(v[j])) * a * s1[j];
-        y[j] = act_f32(z, p.act) * z1 * g;
-      }
-      put16(n0 + c, y);
-    } else {
+  for (int c = 0; c < 32; c += 16) {
+    float y[16], y1[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) y[j] = static_cast<float>(static_cast<int>(u[j])) * a * s0[j] * g;
-      put16(n0 + c, y);
-      if (second) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = static_cast<float>(static_cast<int>(v[j])) * a * s1[j] * g;
-        put16(n0 + c + 16, y);
-      }
+    for (int j = 0; j < 16; ++j) {
+      y[j] = static_cast<float>(static_cast<int>(u[c + j])) * sc[c + j] * (DUAL ? a : ag);
+      y1[j] = static_cast<float>(static_cast<int>(v[c + j])) * sc[32 + c + j] * ag;
     }
+    if (DUAL) {
+      activate(y, p.act);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[j] *= y1[j];
+    }
+    put16(c, y);
+    if (!DUAL) put16(32 + c, y1);
   }
 }
 
+// Arrive on an mbarrier of either CTA, in the default (CTA) scope: what it orders is
+// shared-memory and TMEM reads; a release in cluster scope would also wait for the
+// epilogue's global stores (measured: 4328 x 352 x 5568 gated 76 us with it).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 template <bool DUAL, bool OB>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(PTHREADS, 1)
     moe_int8_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
                          const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -874,7 +930,9 @@ __global__ void __launch_bounds__(256, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* tile_q = abort_flag + 1;
-  int32_t* pre = reinterpret_cast<int32_t*>(full_bar) + 64;
+  float* scales = reinterpret_cast<float*>(full_bar) + 64;
+  int32_t* pre = reinterpret_cast<int32_t*>(scales + PEPI * PSCALES);
+  int32_t* off = pre + p.n_experts + 1;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();  // 0: issues the MMAs of the pair
@@ -885,7 +943,7 @@ __global__ void __launch_bounds__(256, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull_bar[b], 1);
-      mbar_init(&tempty_bar[b], 2 * 4);
+      mbar_init(&tempty_bar[b], 2 * PEPI);
     }
     for (int i = 0; i < PQ; ++i) {
       mbar_init(&qfull_bar[i], 1);
@@ -902,7 +960,10 @@ __global__ void __launch_bounds__(256, 1)
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
-  for (int e = threadIdx.x; e <= p.n_experts; e += 256) pre[e] = p.sched->pre[e];
+  for (int e = threadIdx.x; e <= p.n_experts; e += PTHREADS) {
+    pre[e] = p.sched->pre[e];
+    off[e] = p.sched->off[e];
+  }
   tc_fence_before();
   cluster_sync();  // barriers of both CTAs initialised, TMEM allocated in both
   tc_fence_after();
@@ -918,18 +979,19 @@ __global__ void __launch_bounds__(256, 1)
     const int mt = pre[t.e + 1] - pre[t.e];
     int m, c, ks;
     tile_coords(tile - pre[t.e] * p.nt, mt, p.nt, group_for(mt, p.group_rows, p.group_limit), m, c, ks);
-    t.row0 = p.sched->off[t.e] + m * PAIR_ROWS;
-    t.rows = min(PAIR_ROWS, p.sched->cnt[t.e] - m * PAIR_ROWS);
+    t.row0 = off[t.e] + m * PAIR_ROWS;
+    t.rows = min(PAIR_ROWS, off[t.e + 1] - t.row0);
     t.n0 = c * (DUAL ? 128 : 256);
     return t;
   };
   // Queue operations: the tile id, -1 when none is left, -2 when a wait ran out.
-  auto q_fill = [&](int i) -> int {  // even CTA's producer
+  int ahead = 0;  // even CTA's producer: the tile id taken while the tile before it loads
+  auto q_fill = [&](int i) -> int {
     const int slot = i % PQ;
     const uint32_t ph = (i / PQ) & 1;
     if (!mbar_wait_cluster(&qempty_bar[slot], ph ^ 1) || *abort_flag) return -2;
-    const int t = atomicAdd(p.counters, 1);
-    const int tile = t < ntiles ? t : -1;
+    const int tile = ahead < ntiles ? ahead : -1;
+    if (tile >= 0) ahead = atomicAdd(p.counters, 1);
     tile_q[slot] = tile;
     st_shared_cluster_u32(mapa_shared(const_cast<int*>(&tile_q[slot]), 1), static_cast<uint32_t>(tile));
     mbar_arrive(&qfull_bar[slot]);
@@ -941,7 +1003,7 @@ __global__ void __launch_bounds__(256, 1)
     const uint32_t ph = (i / PQ) & 1;
     if (!mbar_wait_cluster(&qfull_bar[slot], ph) || *abort_flag) return -2;
     const int tile = tile_q[slot];
-    mbar_arrive_cluster(mapa_shared(&qempty_bar[slot], 0));
+    mbar_arrive_remote(mapa_shared(&qempty_bar[slot], 0));
     return tile;
   };
   auto q_take_warp = [&](int i) -> int {  // a whole epilogue warp, one arrive
@@ -951,7 +1013,7 @@ __global__ void __launch_bounds__(256, 1)
     if (!__all_sync(0xffffffffu, ok)) return -2;
     const int tile = tile_q[slot];
     __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(mapa_shared(&qempty_bar[slot], 0));
+    if (lane == 0) mbar_arrive_remote(mapa_shared(&qempty_bar[slot], 0));
     return tile;
   };
 
@@ -960,6 +1022,7 @@ __global__ void __launch_bounds__(256, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
+    if (rank == 0) ahead = atomicAdd(p.counters, 1);
     for (int i = 0; ok; ++i) {
       const int tile = rank == 0 ? q_fill(i) : q_take(i);
       if (tile == -2) ok = false;
@@ -1045,26 +1108,46 @@ __global__ void __launch_bounds__(256, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue --
-    const int q = warp - 4;
+    const int q = warp % 4, set = (warp - 4) / 4;
+    const int c0 = set * (DUAL ? PCOLS / 2 : PCOLS);
+    float* sc = scales + (warp - 4) * PSCALES;
     const uint32_t tempty0[2] = {mapa_shared(&tempty_bar[0], 0), mapa_shared(&tempty_bar[1], 0)};
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int i = 0;; ++i) {
       const int tile = q_take_warp(i);
       if (tile == -1) break;
+      Tile t{};
+      int64_t row = 0;
+      bool valid = false;
+      float a = 0.0f, ag = 0.0f;
+      if (tile >= 0) {  // what the tile needs besides its sums, on its way before they are
+        t = decode(tile);
+        const int r = 128 * static_cast<int>(rank) + 32 * q + lane;
+        row = static_cast<int64_t>(t.row0) + r;
+        valid = r < t.rows;
+        if (valid) {
+          a = __ldg(p.a + row);
+          ag = p.gate != nullptr ? a * __ldg(p.gate + row) : a;
+        }
+        pair_scales<DUAL>(p, t.e, t.n0, c0, lane, sc);
+      }
       if (tile == -2 || !warp_wait(&tfull_bar[acc], acc_phase, abort_flag)) {
         atomicOr(p.status, kStatusEpilogueTimeout);
         *abort_flag = 1;
         break;
       }
       tc_fence_after();
-      const Tile t = decode(tile);
-      const int r = 128 * static_cast<int>(rank) + 32 * q + lane;
-      pair_epilogue<DUAL, OB>(p, t.e, t.n0, tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * 256,
-                              static_cast<int64_t>(t.row0) + r, r < t.rows);
+      // The sums go to registers at once, so that the accumulator is free for the next
+      // tile but one before this one is scaled and stored.
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * 256 + c0;
+      uint32_t u[32], v[32];
+      tmem_ld32x2(tb, tb + (DUAL ? 128 : 32), u, v);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty0[acc]);
+      if (lane == 0) mbar_arrive_remote(tempty0[acc]);
+      if (valid) pair_epilogue<DUAL, OB>(p, t.n0 + c0, u, v, sc, row, a, ag);
+      __syncwarp();  // every lane has read the scales
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1;
@@ -1139,7 +1222,7 @@ template <int ROWS, bool DUAL, bool OB>
 cudaError_t launch_stream(const moe_int8_args_t* a, const void* q, Params p, cudaStream_t s) {
   using C = StreamCfg<ROWS>;
   auto kern = moe_int8_stream_kernel<ROWS, DUAL, OB>;
-  constexpr int kSmem = C::SMEM + (kMaxExperts + 1) * 4;
+  constexpr int kSmem = C::SMEM + 2 * (kMaxExperts + 1) * 4;
   static_assert(kSmem <= 232448, "shared memory above the per-block limit");
   static_assert((2 * C::STAGES + 5) * 8 + 16 <= 256, "barrier area too small");
   const cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), kSmem);
@@ -1165,7 +1248,7 @@ cudaError_t launch_pair(const moe_int8_args_t* a, const void* q, Params p, cudaS
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.blockDim = dim3(PTHREADS, 1, 1);
   cfg.dynamicSmemBytes = PSMEM;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -1179,7 +1262,7 @@ cudaError_t launch_pair(const moe_int8_args_t* a, const void* q, Params p, cudaS
     at.val.clusterDim.z = 1;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3(2 * (device_sm_count() / 2), 1, 1);
-    c.blockDim = dim3(256, 1, 1);
+    c.blockDim = dim3(PTHREADS, 1, 1);
     c.dynamicSmemBytes = PSMEM;
     c.attrs = &at;
     c.numAttrs = 1;
@@ -1210,8 +1293,9 @@ cudaError_t launch_prepare_ring(const PrepParams& p, int32_t ring, cudaStream_t 
   return cudaGetLastError();
 }
 
-// Threads per row: the fewest whose registers hold it (a warp for K <= 1024, 256
-// threads for K <= 8192), as long as two rows of every group fit in shared memory.
+// Threads per row: the fewest whose registers hold it (a warp for K <= 2048, 128 threads
+// for K <= 8192, 256 for K <= 16384, 512 for K <= 32768), as long as two rows of every group fit in
+// shared memory.
 template <bool BF16>
 cudaError_t launch_prepare(const PrepParams& p, cudaStream_t s) {
   auto ring = [&](int nt) -> int32_t {
@@ -1219,10 +1303,11 @@ cudaError_t launch_prepare(const PrepParams& p, cudaStream_t s) {
     const int64_t rows = kRingBytes / (p.K * (BF16 ? 2 : 4)) / (kPrepCta / nt);
     return rows < 2 ? 0 : static_cast<int32_t>(std::min<int64_t>(rows, kRing));
   };
-  if (!p.quantise) return launch_prepare_ring<BF16, 1024>(p, 0, s);
+  if (!p.quantise) return launch_prepare_ring<BF16, 512>(p, 0, s);
   if (const int32_t n = ring(32)) return launch_prepare_ring<BF16, 32>(p, n, s);
+  if (const int32_t n = ring(128)) return launch_prepare_ring<BF16, 128>(p, n, s);
   if (const int32_t n = ring(256)) return launch_prepare_ring<BF16, 256>(p, n, s);
-  if (const int32_t n = ring(1024)) return launch_prepare_ring<BF16, 1024>(p, n, s);
+  if (const int32_t n = ring(512)) return launch_prepare_ring<BF16, 512>(p, n, s);
   moe_int8_prepare_long_kernel<BF16><<<static_cast<unsigned>(1 + p.R), kPrepCta, 0, s>>>(p);
   return cudaGetLastError();
 }
