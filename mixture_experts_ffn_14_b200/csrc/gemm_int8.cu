@@ -34,6 +34,10 @@ constexpr int BK = 128;              // K per stage: 128 bytes = one swizzle row
 constexpr int WBOX = BK * 128;       // 16 KB: [128 K x 128 columns]
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxCtas = 160;        // product CTAs at most (workspace sizing; 148 SMs on B200)
+// Split form: CTAs per tile, and the clusters of that many that run at once with a margin
+// of one (one CTA per SM: 15, 22, 26, 33, 45 and 74 fit on the eight GPCs of a B200). One
+// cluster more is a second wave: 16 x 4096 x 4096, 16 tiles in clusters of 8: 18 us, of 4: 9.
+constexpr int kSplits[6][2] = {{8, 14}, {6, 21}, {5, 25}, {4, 32}, {3, 44}, {2, 73}};
 
 // Tile schedule in the workspace, made by the prepare kernel.
 struct Sched {
@@ -310,6 +314,7 @@ __global__ void __launch_bounds__(kPrepCta, 1)
   __shared__ __align__(8) uint64_t full[GROUPS][kRing];
   __shared__ int real_row[GROUPS][kRing];
   __shared__ uint32_t part[GROUPS][2][WARPS < 32 ? 32 : WARPS];
+  launch_dependents();
   if (blockIdx.x == gridDim.x - 1 && threadIdx.x < kPrepThreads) make_schedule(p);
   if (!p.quantise) return;
   const int group = threadIdx.x / NT, tid = threadIdx.x % NT, lane = threadIdx.x % 32, warp = tid / 32;
@@ -388,6 +393,7 @@ __global__ void __launch_bounds__(kPrepCta, 1)
 template <bool BF16>
 __global__ void __launch_bounds__(kPrepCta) moe_int8_prepare_long_kernel(const __grid_constant__ PrepParams p) {
   __shared__ uint32_t part[kPrepCta / 32];
+  launch_dependents();
   if (blockIdx.x == 0) {
     if (threadIdx.x < kPrepThreads) make_schedule(p);
     return;
@@ -415,6 +421,7 @@ __global__ void __launch_bounds__(kPrepCta) moe_int8_prepare_long_kernel(const _
 
 struct Params {
   const Sched* sched;
+  const int32_t* counts; // [n_experts] or nullptr: all R rows (split form of up to 32 experts)
   const float* a;        // [R] row scales
   const float* gate;     // [R] or nullptr
   const __nv_bfloat16* s0;
@@ -486,11 +493,11 @@ struct StreamCfg {
   static constexpr int STAGES = ROWS <= 64 ? 5 : 4;
   static constexpr int ACC_COLS = 2 * ROWS;  // two 128-column blocks of weights
   static constexpr int TMEM_COLS = 2 * ACC_COLS;
-  static constexpr int PART_INTS = 256 * ROWS;
+  static constexpr int PART_INTS = 256 * ROWS;  // of a part: [16-token step][8][column][4], see the epilogue
   static constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 256;  // alignment slack, barriers; + schedule
 };
 constexpr int XBOX_ROWS = 32;
-constexpr int kMinRun = 8;  // K blocks of a run at least: 1024 of K
+constexpr int kMinRun = 4;  // K blocks of a run at least: 512 of K
 
 struct Seg {
   int e, row0, rows, n0, kb0, kb1;
@@ -722,12 +729,12 @@ __global__ void __launch_bounds__(256, 1)
         for (int j0 = 0; j0 < s.rows; j0 += 16) {
           uint32_t u[16], v[16];
           tmem_ld16x2(tb + j0, tb + ROWS + j0, u, v);
+          int4* o = reinterpret_cast<int4*>(mine) + (j0 / 16) * 8 * 128 + col;
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (j0 + j < s.rows) {
-              __stcg(mine + (j0 + j) * 256 + col, static_cast<int>(u[j]));
-              __stcg(mine + (j0 + j) * 256 + 128 + col, static_cast<int>(v[j]));
-            }
+          for (int i = 0; i < 4; ++i) {
+            __stcg(o + i * 128, make_int4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]));
+            __stcg(o + (4 + i) * 128, make_int4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          }
         }
         __threadfence();
         asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -746,16 +753,20 @@ __global__ void __launch_bounds__(256, 1)
           uint32_t u[16], v[16];
           tmem_ld16x2(tb + j0, tb + ROWS + j0, u, v);
           if (!whole) {
-#pragma unroll 1
+            // the other CTAs' parts, two of them on their way at a time
+#pragma unroll 2
             for (int c = first; c <= last; ++c) {
               if (c == me) continue;
-              const int32_t* o = p.part + (2 * static_cast<int64_t>(c) + (c == first ? 1 : 0)) * C::PART_INTS;
+              const int4* o = reinterpret_cast<const int4*>(p.part + (2 * static_cast<int64_t>(c) + (c == first ? 1 : 0)) *
+                                                                         C::PART_INTS) + (j0 / 16) * 8 * 128 + col;
+              int4 w[8];
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (j0 + j < s.rows) {
-                  u[j] += static_cast<uint32_t>(__ldcg(o + (j0 + j) * 256 + col));
-                  v[j] += static_cast<uint32_t>(__ldcg(o + (j0 + j) * 256 + 128 + col));
-                }
+              for (int i = 0; i < 8; ++i) w[i] = __ldcg(o + i * 128);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                u[4 * i] += w[i].x; u[4 * i + 1] += w[i].y; u[4 * i + 2] += w[i].z; u[4 * i + 3] += w[i].w;
+                v[4 * i] += w[4 + i].x; v[4 * i + 1] += w[4 + i].y; v[4 * i + 2] += w[4 + i].z; v[4 * i + 3] += w[4 + i].w;
+              }
             }
           }
           float za[16], zb[16];
@@ -800,6 +811,265 @@ __global__ void __launch_bounds__(256, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// The schedule of up to 32 experts by one warp, from the counts themselves (a lane
+// each), cut off as make_schedule cuts them off. `report`: write the status word, too.
+__device__ __forceinline__ void warp_schedule(const Params& p, int tile_rows, int32_t* pre, int32_t* off, bool report) {
+  const int lane = threadIdx.x % 32;
+  long long c = 0;
+  if (lane < p.n_experts) c = p.counts != nullptr ? p.counts[lane] : p.R;
+  const bool negative = c < 0;
+  if (negative) c = 0;
+  long long end = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, end, o);
+    if (lane >= o) end += v;
+  }
+  const int first = static_cast<int>(min(end - c, static_cast<long long>(p.R)));
+  const int last = static_cast<int>(min(end, static_cast<long long>(p.R)));
+  const int tiles = (last - first + tile_rows - 1) / tile_rows;
+  int tend = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, tend, o);
+    if (lane >= o) tend += v;
+  }
+  if (lane < p.n_experts) {
+    pre[lane] = tend - tiles;
+    off[lane] = first;
+  }
+  if (lane == p.n_experts - 1) {
+    pre[p.n_experts] = tend;
+    off[p.n_experts] = last;
+  }
+  const bool bad = __any_sync(0xffffffffu, negative || last - first < c);
+  if (report && lane == 0) *p.status = bad ? kStatusBounds : 0u;
+}
+
+// ---- split form --------------------------------------------------------------
+// For products with few tiles, where time is latency: a
+// cluster of S CTAs takes one tile, each a run of its K blocks; the partial sums meet in
+// shared memory, and every CTA adds and finishes each S-th row from its peers' memory.
+// (In the stream form one CTA joined the parts from L2: 64 x 4096 x 4096 took 20-25 us.)
+
+template <int ROWS, bool DUAL, bool OB>
+__global__ void __launch_bounds__(256, 1)
+    moe_int8_split_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
+                          const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ Params p, int32_t S) {
+  using C = StreamCfg<ROWS>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES);
+  uint64_t* empty_bar = full_bar + C::STAGES;
+  uint64_t* tfull_bar = empty_bar + C::STAGES;
+  uint64_t* drain_bar = tfull_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* pre = reinterpret_cast<int32_t*>(full_bar) + 64;
+  int32_t* off = pre + p.n_experts + 1;
+  int32_t* part = reinterpret_cast<int32_t*>(smem);  // [ROWS][256] sums, once the ring is done with
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rank = static_cast<int>(cluster_ctarank());
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    mbar_init(tfull_bar, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_w0);
+    if (DUAL) tma_prefetch_desc(&tm_w1);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::ACC_COLS);
+    tmem_relinquish();
+  }
+  if (p.n_experts <= 32) {
+    if (warp == 2) warp_schedule(p, ROWS, pre, off, blockIdx.x == 0);
+    wait_prerequisites();  // the quantised rows
+  } else {
+    wait_prerequisites();  // the schedule and the quantised rows
+    for (int e = threadIdx.x; e <= p.n_experts; e += 256) {
+      pre[e] = p.sched->pre[e];
+      off[e] = p.sched->off[e];
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int tile = static_cast<int>(blockIdx.x / S);
+  if (tile < pre[p.n_experts] * p.nt) {  // the same for the whole cluster
+    const int e = expert_of(pre, p.n_experts, tile / p.nt);
+    const int mt = pre[e + 1] - pre[e], local = tile - pre[e] * p.nt;
+    const int n0 = (local / mt) * (DUAL ? 128 : 256);
+    const int row0 = off[e] + (local % mt) * ROWS;
+    const int rows = min(ROWS, off[e + 1] - row0);
+    const int kb0 = p.kb * rank / S, kb1 = p.kb * (rank + 1) / S;
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer --
+      const uint64_t wpolicy = policy_evict_first();
+      const int boxes = (rows + XBOX_ROWS - 1) / XBOX_ROWS;
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&empty_bar[stage], phase ^ 1, kWaitLimitNs) || *abort_flag) {
+          atomicOr(p.status, kStatusProducerTimeout);
+          *abort_flag = 1;
+          for (int i = 0; i < min(issued, C::STAGES); ++i) {  // no copy may still be on its way
+            if (--stage < 0) {
+              stage = C::STAGES - 1;
+              phase ^= 1;
+            }
+            mbar_wait(&full_bar[stage], phase, kWaitLimitNs);
+          }
+          break;
+        }
+        uint8_t* xs = smem + stage * C::STAGE_BYTES;
+        uint8_t* ws = xs + C::X_BYTES;
+        mbar_arrive_expect_tx(&full_bar[stage], boxes * XBOX_ROWS * BK + 2 * WBOX);
+        tma_load_3d_hint(ws, &tm_w0, &full_bar[stage], n0, kb * BK, e, wpolicy);
+        tma_load_3d_hint(ws + WBOX, DUAL ? &tm_w1 : &tm_w0, &full_bar[stage], DUAL ? n0 : n0 + 128, kb * BK, e, wpolicy);
+        for (int b = 0; b < boxes; ++b)
+          tma_load_2d(xs + b * XBOX_ROWS * BK, &tm_x, &full_bar[stage], kb * BK, row0 + b * XBOX_ROWS);
+        ++issued;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    } else if (warp == 1 && lane == 0) {
+      // --------------------------------------------------------------- MMA --
+      const uint32_t idesc = idesc_s8_s32(128, (rows + 31) / 32 * 32, 1, 0);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&full_bar[stage], phase, kWaitLimitNs) || *abort_flag) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t xs = smem_u32(smem + stage * C::STAGE_BYTES);
+        const uint32_t ws = xs + C::X_BYTES;
+#pragma unroll
+        for (int k = 0; k < BK / 32; ++k) {  // operand layouts as in the stream form
+          const uint32_t accum = kb > kb0 || k > 0;
+          const uint64_t xd = smem_desc_sw128(xs + k * 32, 16, 1024);
+          umma_s8(tmem_base, smem_desc_sw128(ws + k * 4096, WBOX, 1024), xd, idesc, accum);
+          umma_s8(tmem_base + ROWS, smem_desc_sw128(ws + WBOX + k * 4096, WBOX, 1024), xd, idesc, accum);
+        }
+        umma_commit(&empty_bar[stage]);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (ok) {
+        umma_commit(tfull_bar);
+      } else {
+        atomicOr(p.status, kStatusMmaTimeout);
+        *abort_flag = 1;
+        umma_commit(drain_bar);  // unwinding: the tensor cores are done before TMEM is freed
+        mbar_wait(drain_bar, 0, kWaitLimitNs);
+      }
+    } else if (warp >= 4) {
+      // ---------------------------------------------------- sums to shared --
+      // Every load of the ring has been consumed once the last MMA is complete.
+      if (warp_wait(tfull_bar, 0, abort_flag)) {
+        tc_fence_after();
+        const int q = warp - 4, col = 32 * q + lane;
+        const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+#pragma unroll 1
+        for (int j0 = 0; j0 < rows; j0 += 16) {
+          uint32_t u[16], v[16];
+          tmem_ld16x2(tb + j0, tb + ROWS + j0, u, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            part[(j0 + j) * 256 + col] = static_cast<int>(u[j]);
+            part[(j0 + j) * 256 + 128 + col] = static_cast<int>(v[j]);
+          }
+        }
+        tc_fence_before();
+      } else {
+        atomicOr(p.status, kStatusEpilogueTimeout);
+        *abort_flag = 1;
+      }
+    }
+    // What the finish needs besides the sums, on its way meanwhile.
+    const int c = threadIdx.x % 128, half = threadIdx.x / 128;
+    const int ca = n0 + c, cb = DUAL ? ca : ca + 128;
+    const bool va = ca < p.N, vb = cb < p.N;
+    const int64_t se = static_cast<int64_t>(e) * p.N;
+    const float sa = va ? __bfloat162float(p.s0[se + ca]) : 0.0f;
+    const float sb = vb ? __bfloat162float((DUAL ? p.s1 : p.s0)[se + cb]) : 0.0f;
+    __syncwarp();
+    cluster_sync();  // every CTA's sums are in its shared memory
+    constexpr int kAtOnce = 4;  // rows whose remote loads are on their way together
+    for (int r0 = rank + S * half; r0 < rows; r0 += 2 * S * kAtOnce) {
+      int32_t w[kAtOnce][2] = {};
+      float a[kAtOnce], ag[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int r = min(r0 + 2 * S * k, rows - 1);
+        const int64_t row = static_cast<int64_t>(row0) + r;
+        a[k] = __ldg(p.a + row);
+        ag[k] = p.gate != nullptr ? __ldg(p.gate + row) : 1.0f;
+      }
+      for (int i = 0; i < S; ++i) {
+        const uint32_t base = mapa_shared(part, i) + c * 4;
+        int32_t t[kAtOnce][2];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const uint32_t at = base + min(r0 + 2 * S * k, rows - 1) * 1024;
+          t[k][0] = ld_shared_cluster_s32(at);
+          t[k][1] = ld_shared_cluster_s32(at + 512);
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          w[k][0] += t[k][0];
+          w[k][1] += t[k][1];
+        }
+      }
+      float za[kAtOnce], zb[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        ag[k] *= a[k];
+        za[k] = static_cast<float>(w[k][0]) * sa * (DUAL ? a[k] : ag[k]);
+        zb[k] = static_cast<float>(w[k][1]) * sb * ag[k];
+      }
+      if (DUAL) {
+        activate(za, p.act);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) za[k] *= zb[k];
+      }
+      auto put = [&](auto* out) {
+        using T = std::remove_pointer_t<decltype(out)>;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int r = r0 + 2 * S * k;
+          T* o = out + (static_cast<int64_t>(row0) + r) * p.N;
+          if (r < rows && va) o[ca] = static_cast<T>(za[k]);
+          if (!DUAL && r < rows && vb) o[cb] = static_cast<T>(zb[k]);
+        }
+      };
+      if (OB) put(static_cast<__nv_bfloat16*>(p.out));
+      else put(static_cast<float*>(p.out));
+    }
+    cluster_sync();  // no CTA leaves while another may read its sums
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::ACC_COLS);
   }
 }
 
@@ -1167,10 +1437,20 @@ __global__ void __launch_bounds__(PTHREADS, 1)
 
 struct Layout {
   size_t status, sched, counters, q, a, part, total;
-  int32_t tile_rows;  // rows of a tile: 64 or 128 (stream form), 256 (pair form)
+  int32_t tile_rows;  // rows of a tile: 64 or 128 (stream and split form), 256 (pair form)
+  int32_t split;      // CTAs per tile of the split form, 0: another form
 };
 
-Layout plan(int64_t R, int64_t K, int32_t n_experts, moe_dtype_t x_dtype) {
+// Which form, from the sizes alone (the rows of each expert are only known on the device):
+// - split form if the tiles there can be at most leave room for two CTAs or more each (us,
+//   split against stream or pair form: 16 x 4096 x 4096 9.0 and 11.6, 64 rows 10.7 and
+//   20-25, 128 rows 13.1 and 28-39, 333 rows 18.4 and 33.8), unless few CTAs would have
+//   long runs (16 x 14336 x 4096: 28 K blocks on 64 CTAs 19.2, stream form 17.5);
+// - else by the rows an expert has on average: up to 48 the stream form in tiles of 64, up
+//   to 128 in tiles of 128, above them the pair form. Measured at the Grok-1 shape,
+//   gate/up and down, us: 128 rows per expert, stream 612 and 259, pair 698 and 339; 192,
+//   stream 1078, pair 705.
+Layout plan(int64_t R, int64_t K, int64_t N, int32_t n_experts, moe_dtype_t x_dtype, bool dual) {
   Layout L{};
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -1178,7 +1458,15 @@ Layout plan(int64_t R, int64_t K, int32_t n_experts, moe_dtype_t x_dtype) {
     o = (o + bytes + 255) / 256 * 256;
     return at;
   };
-  L.tile_rows = R <= 48 * static_cast<int64_t>(n_experts) ? 64 : (R <= 96 * static_cast<int64_t>(n_experts) ? 128 : 256);
+  const int64_t kb = (K + BK - 1) / BK, nt = (N + (dual ? 127 : 255)) / (dual ? 128 : 256);
+  L.tile_rows = R <= 48 * static_cast<int64_t>(n_experts) || R <= 64 ? 64 : 128;
+  // an expert's last tile may be short: at most one more row tile for each but one
+  const int64_t tiles = std::min<int64_t>(R, (R + L.tile_rows - 1) / L.tile_rows + n_experts - 1) * nt;
+  for (const auto& s : kSplits)
+    if (L.split == 0 && tiles <= s[1] && kb >= 2 * s[0]) L.split = s[0];
+  if (L.split > 0 && tiles * L.split < 96 && kb > 24 * L.split && R <= 128 * static_cast<int64_t>(n_experts))
+    L.split = 0;
+  if (L.split == 0 && R > 128 * static_cast<int64_t>(n_experts)) L.tile_rows = PAIR_ROWS;
   L.status = take(256);
   L.sched = take(sizeof(Sched));
   L.counters = take(sizeof(int32_t) * kMaxCtas);
@@ -1187,7 +1475,7 @@ Layout plan(int64_t R, int64_t K, int32_t n_experts, moe_dtype_t x_dtype) {
     L.a = take(sizeof(float) * R);
   }
   L.part = o;
-  if (L.tile_rows < PAIR_ROWS) take(sizeof(int32_t) * 2 * kMaxCtas * 256 * static_cast<size_t>(L.tile_rows));
+  if (L.tile_rows < PAIR_ROWS && L.split == 0) take(sizeof(int32_t) * 2 * kMaxCtas * 256 * static_cast<size_t>(L.tile_rows));
   L.total = o;
   return L;
 }
@@ -1218,23 +1506,31 @@ bool row_map(CUtensorMap* m, const void* q, const moe_int8_args_t* a, uint32_t b
   return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Stream form, or split form with `split` CTAs per tile.
 template <int ROWS, bool DUAL, bool OB>
-cudaError_t launch_stream(const moe_int8_args_t* a, const void* q, Params p, cudaStream_t s) {
+cudaError_t launch_stream(const moe_int8_args_t* a, const void* q, Params p, int32_t split, bool dependent,
+                          cudaStream_t s) {
   using C = StreamCfg<ROWS>;
   auto kern = moe_int8_stream_kernel<ROWS, DUAL, OB>;
+  auto split_kern = moe_int8_split_kernel<ROWS, DUAL, OB>;
   constexpr int kSmem = C::SMEM + 2 * (kMaxExperts + 1) * 4;
   static_assert(kSmem <= 232448, "shared memory above the per-block limit");
   static_assert((2 * C::STAGES + 5) * 8 + 16 <= 256, "barrier area too small");
-  const cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), kSmem);
+  const cudaError_t err = set_smem_limit_once(split > 0 ? reinterpret_cast<const void*>(split_kern)
+                                                        : reinterpret_cast<const void*>(kern), kSmem);
   if (err != cudaSuccess) return err;
   CUtensorMap tx, tw0, tw1;
   if (!row_map(&tx, q, a, XBOX_ROWS) || !weight_map(&tw0, a->w, a) || !weight_map(&tw1, DUAL ? a->w_up : a->w, a))
     return cudaErrorInvalidValue;
   p.nt = static_cast<int32_t>((a->N + (DUAL ? 127 : 255)) / (DUAL ? 128 : 256));
+  if (split > 0) {
+    const int64_t tiles = std::min<int64_t>(a->R, (a->R + ROWS - 1) / ROWS + a->n_experts - 1) * p.nt;
+    return launch_kernel(split_kern, static_cast<unsigned>(tiles * split), 256, kSmem, s, split, dependent, tx, tw0, tw1, p,
+                         split);
+  }
   const int64_t most = ((a->R + ROWS - 1) / ROWS + a->n_experts) * p.nt * p.kb;
   const int grid = static_cast<int>(std::min<int64_t>(std::min(device_sm_count(), kMaxCtas), most));
-  kern<<<grid, 256, kSmem, s>>>(tx, tw0, tw1, p);
-  return cudaGetLastError();
+  return launch_kernel(kern, grid, 256, kSmem, s, 1, false, tx, tw0, tw1, p);
 }
 
 template <bool DUAL, bool OB>
@@ -1242,17 +1538,6 @@ cudaError_t launch_pair(const moe_int8_args_t* a, const void* q, Params p, cudaS
   auto kern = moe_int8_pair_kernel<DUAL, OB>;
   const cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), PSMEM);
   if (err != cudaSuccess) return err;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(PTHREADS, 1, 1);
-  cfg.dynamicSmemBytes = PSMEM;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   // Clusters of two that fit at once on this device (queried once per device).
   const int max_pairs = once_per_device(reinterpret_cast<const void*>(&launch_pair<DUAL, OB>), [](const void*) {
     cudaLaunchAttribute at;
@@ -1278,8 +1563,8 @@ cudaError_t launch_pair(const moe_int8_args_t* a, const void* q, Params p, cudaS
   p.group_rows = row_group_size(PAIR_ROWS, (a->K + 1) / 2, tc::kL2GroupBytes);
   p.group_limit = row_group_size(PAIR_ROWS, (a->K + 1) / 2, tc::kL2UngroupedBytes);
   const int64_t most = ((a->R + PAIR_ROWS - 1) / PAIR_ROWS + a->n_experts) * p.nt;
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(most, max_pairs)), 1, 1);
-  return cudaLaunchKernelEx(&cfg, kern, tx, tw0, tw1, p);
+  return launch_kernel(kern, 2 * static_cast<unsigned>(std::min<int64_t>(most, max_pairs)), PTHREADS, PSMEM, s, 2, false,
+                       tx, tw0, tw1, p);
 }
 
 template <bool BF16, int NT>
@@ -1322,7 +1607,7 @@ extern "C" {
 size_t moe_int8_workspace_size(int64_t R, int64_t K, int64_t N, int32_t n_experts, moe_dtype_t x_dtype,
                                int32_t with_up) {
   if (R <= 0 || (with_up != 0 && with_up != 1) || i8::check_sizes(R, K, N, n_experts, x_dtype) != MOE_OK) return 0;
-  return i8::plan(R, K, n_experts, x_dtype).total;
+  return i8::plan(R, K, N, n_experts, x_dtype, with_up == 1).total;
 }
 
 moe_status_t moe_int8_product(const moe_int8_args_t* a, void* workspace, size_t ws_bytes, moe_stream_t stream) {
@@ -1340,7 +1625,7 @@ moe_status_t moe_int8_product(const moe_int8_args_t* a, void* workspace, size_t 
   const void* const all[] = {a->x, a->x_scale, a->index, a->counts, a->w, a->w_up, a->s, a->s_up, a->gate, a->out};
   for (const void* q : all)
     if (!i8::aligned16(q)) return MOE_ERR_MISALIGNED;
-  const i8::Layout L = i8::plan(a->R, a->K, a->n_experts, a->x_dtype);
+  const i8::Layout L = i8::plan(a->R, a->K, a->N, a->n_experts, a->x_dtype, dual);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < L.total)
     return MOE_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1361,11 +1646,16 @@ moe_status_t moe_int8_product(const moe_int8_args_t* a, void* workspace, size_t 
   pp.sched = reinterpret_cast<i8::Sched*>(ws + L.sched);
   pp.counters = reinterpret_cast<int32_t*>(ws + L.counters);
   pp.status = reinterpret_cast<uint32_t*>(ws + L.status);
-  if ((a->x_dtype == MOE_F32 ? i8::launch_prepare<false>(pp, s) : i8::launch_prepare<true>(pp, s)) != cudaSuccess)
+  // Rows that are 8-bit already need nothing prepared where the product kernel makes
+  // its own schedule.
+  const bool prepared = !rows8 || L.split == 0 || a->n_experts > 32;
+  if (prepared &&
+      (a->x_dtype == MOE_F32 ? i8::launch_prepare<false>(pp, s) : i8::launch_prepare<true>(pp, s)) != cudaSuccess)
     return MOE_ERR_CUDA;
 
   i8::Params p{};
   p.sched = pp.sched;
+  p.counts = a->counts;
   p.a = rows8 ? a->x_scale : pp.a;
   p.gate = a->gate;
   p.s0 = static_cast<const __nv_bfloat16*>(a->s);
@@ -1383,8 +1673,11 @@ moe_status_t moe_int8_product(const moe_int8_args_t* a, void* workspace, size_t 
   const bool ob = a->out_dtype == MOE_BF16;
   auto form = [&](auto rows) {
     constexpr int ROWS = decltype(rows)::value;
-    if (dual) return ob ? i8::launch_stream<ROWS, true, true>(a, q, p, s) : i8::launch_stream<ROWS, true, false>(a, q, p, s);
-    return ob ? i8::launch_stream<ROWS, false, true>(a, q, p, s) : i8::launch_stream<ROWS, false, false>(a, q, p, s);
+    if (dual)
+      return ob ? i8::launch_stream<ROWS, true, true>(a, q, p, L.split, prepared, s)
+                : i8::launch_stream<ROWS, true, false>(a, q, p, L.split, prepared, s);
+    return ob ? i8::launch_stream<ROWS, false, true>(a, q, p, L.split, prepared, s)
+              : i8::launch_stream<ROWS, false, false>(a, q, p, L.split, prepared, s);
   };
   cudaError_t e;
   if (L.tile_rows == 64) e = form(std::integral_constant<int, 64>{});

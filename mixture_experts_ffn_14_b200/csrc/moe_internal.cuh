@@ -164,6 +164,34 @@ int device_sm_count();
 // A negative result is an error and is not cached.
 int once_per_device(const void* key, int (*setup)(const void* key));
 
+// Host: launch a kernel in clusters of `cluster` CTAs (1 = none); `dependent`: it calls
+// wait_prerequisites() before it touches what the kernel before it writes, so it may be
+// set up while that one runs.
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                          unsigned cluster, bool dependent, const A&... args) {
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  if (dependent) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 // Host: raise a kernel's dynamic shared-memory limit once per device.
 cudaError_t set_smem_limit_once(const void* kern, int bytes);
 

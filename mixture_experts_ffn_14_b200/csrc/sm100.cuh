@@ -129,6 +129,13 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// ------------------------------------------------- dependent launches --
+// Programmatic dependent launch: the next kernel of the stream may start (its set-up
+// overlaps this one) ...
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// ... and waits here until the kernels before it have ended and their writes are visible.
+__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // --------------------------------------------------------------------- TMEM --
 
 // Whole warp: allocate `ncols` TMEM columns (power of two >= 32); the base
