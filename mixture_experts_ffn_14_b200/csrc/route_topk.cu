@@ -747,6 +747,7 @@ __global__ void __launch_bounds__(NW * 32, VPL <= 8 ? 32 / NW : 1)
   __shared__ int part[NW];
   __shared__ int picks[kTopkBlock][32];
   __shared__ float tops[kTopkBlock], sums[kTopkBlock];
+  sm100::launch_dependents();  // the scan may be set up meanwhile
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTopkBlock;
   const int64_t n = token_count(p);
@@ -821,6 +822,8 @@ __global__ void __launch_bounds__(NW * 32, VPL <= 8 ? 32 / NW : 1)
 // expert x, the runs are joined through shared memory.
 __global__ void __launch_bounds__(1024) moe_topk_scan_kernel(const TopkParams p) {
   __shared__ int run[32][33];
+  sm100::launch_dependents();
+  sm100::wait_prerequisites();  // the blocks' histograms
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   const int x = threadIdx.x % 32, y = threadIdx.x / 32;
   const int e = blockIdx.x * 32 + x;
@@ -864,6 +867,7 @@ __global__ void __launch_bounds__(kDispatchWarps * 32) moe_topk_dispatch_kernel(
   __shared__ int part[kDispatchWarps];
   const int64_t blk = blockIdx.x;
   for (int e = threadIdx.x; e < p.E; e += kDispatchWarps * 32) mask[e] = 0;
+  sm100::wait_prerequisites();  // the scan, which has waited for the routing
   block_prefix<kDispatchWarps>(p.E, pre, part, [&](int e) { return p.totals[e]; });
   const int64_t t0 = blk * kTopkBlock;
   const int tokens = static_cast<int>(p.T - t0 < kTopkBlock ? p.T - t0 : kTopkBlock);
@@ -1130,29 +1134,18 @@ moe_status_t moe_topk_route(const moe_topk_args_t* a, const moe_topk_routed_t* r
     constexpr int WIDE = VPL <= 8 ? 32 : 16;
     const int run = p.group_size / VPL;
     p.lane_run = p.group_size % VPL == 0 && (run & (run - 1)) == 0 ? run : 0;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster ? grid : 1;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(few ? WIDE * 32 : 8 * 32, 1, 1);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster ? 1 : 0;
+    const unsigned threads = few ? WIDE * 32 : 8 * 32, blocks = cluster ? grid : 1;
     if (a->dtype == MOE_BF16)
-      return few ? cudaLaunchKernelEx(&cfg, moe_topk_route_kernel<true, VPL, WIDE>, p)
-                 : cudaLaunchKernelEx(&cfg, moe_topk_route_kernel<true, VPL, 8>, p);
-    return few ? cudaLaunchKernelEx(&cfg, moe_topk_route_kernel<false, VPL, WIDE>, p)
-               : cudaLaunchKernelEx(&cfg, moe_topk_route_kernel<false, VPL, 8>, p);
+      return few ? launch_kernel(moe_topk_route_kernel<true, VPL, WIDE>, grid, threads, 0, s, blocks, false, p)
+                 : launch_kernel(moe_topk_route_kernel<true, VPL, 8>, grid, threads, 0, s, blocks, false, p);
+    return few ? launch_kernel(moe_topk_route_kernel<false, VPL, WIDE>, grid, threads, 0, s, blocks, false, p)
+               : launch_kernel(moe_topk_route_kernel<false, VPL, 8>, grid, threads, 0, s, blocks, false, p);
   });
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   if (ws) {
-    moe_topk_scan_kernel<<<(a->E + 31) / 32, 1024, 0, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-    moe_topk_dispatch_kernel<<<grid, kDispatchWarps * 32, 0, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    if (launch_kernel(moe_topk_scan_kernel, (a->E + 31) / 32, 1024, 0, s, 1, true, p) != cudaSuccess ||
+        launch_kernel(moe_topk_dispatch_kernel, grid, kDispatchWarps * 32, 0, s, 1, true, p) != cudaSuccess)
+      return MOE_ERR_CUDA;
   }
   return MOE_OK;
 }
