@@ -16,8 +16,8 @@
 // The choice is that of the 64-bit values. What a key may be off by is known (`err`: the
 // bits given to the index, and with a bias the fp32 rounding of score + bias, derived
 // at score_error); a round whose winner is less than 2 err ahead of the next value, or
-// a group limit that close, is undecided, and that token is chosen again from
-// 64-bit values. With normal logits that is about one token in a hundred. Logits of
+// a group limit that close, is undecided, and those experts are compared again in 64
+// bits. With normal logits that is about one token in a hundred. Logits of
 // few mantissa bits (bf16 ones) lose nothing to the index and are decided exactly.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -176,14 +176,138 @@ constexpr uint32_t kNoKey = 0;
 // for experts that cannot be chosen.
 constexpr uint32_t kFirstKey = 0x00800000u;
 
-// Register j of an array, j not a constant (the array stays in registers).
+// ---- 64-bit values -------------------------------------------------------------
+// Near ties are decided on 64-bit keys that sort like doubles. One such token can be the
+// last of its kernel, so its own time counts (it was 10 us of 35 for 16384 tokens of 256
+// experts while every expert was scored again), and much of that is fetching instructions
+// that no cache holds: only the experts in question are scored again, by one shared
+// function, a lane each, and what must look at all experts keeps its loops rolled.
+
+// 64-bit score of a logit (softmax: the logit less the row's largest; z: the row's sum).
+__device__ __noinline__ double exact_score(int score, double x, double z) {
+  const bool soft = score == MOE_SCORE_SOFTMAX;
+  const double e = exp(soft ? x : -x);
+  return (soft ? e : 1.0) / (soft ? z : 1.0 + e);
+}
+
+// What a token's 64-bit values take besides the logit.
+struct ExactRow {
+  double top = 0.0, z = 1.0;  // softmax: the largest logit and the sum
+};
+
+template <bool BF16, int VPL>
+__device__ __noinline__ ExactRow exact_row(const TopkParams& p, int64_t t, int lane) {
+  ExactRow r;
+  if (p.score != MOE_SCORE_SOFTMAX) return r;
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int e = lane; e < p.E; e += 32) m = fmaxf(m, load_logit<BF16>(p.logits, t * p.E + e));
+  m = warp_max(m);
+  if (m > -INFINITY) r.top = static_cast<double>(m);
+  r.z = 0.0;
+#pragma unroll 1
+  for (int e = lane; e < p.E; e += 32)
+    r.z += exact_score(MOE_SCORE_SOFTMAX, static_cast<double>(load_logit<BF16>(p.logits, t * p.E + e)) - r.top, 1.0);
+  r.z = warp_add(r.z);
+  return r;
+}
+
+// 64-bit value of expert e of token t: score + bias, or the logit.
+template <bool BF16>
+__device__ __forceinline__ double exact_value(const TopkParams& p, int64_t t, int e, bool by_score, const ExactRow& r) {
+  const double x = static_cast<double>(load_logit<BF16>(p.logits, t * p.E + e));
+  if (!by_score) return x;
+  const double s = exact_score(p.score, p.score == MOE_SCORE_SOFTMAX ? x - r.top : x, r.z);
+  return p.bias != nullptr ? s + static_cast<double>(__ldg(p.bias + e)) : s;
+}
+
+__device__ __forceinline__ uint64_t order_key64(double v) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+  return b ^ (static_cast<uint64_t>(static_cast<int64_t>(b) >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double key_value64(uint64_t k) {
+  return __longlong_as_double(
+      static_cast<long long>(k & 0x8000000000000000ull ? k ^ 0x8000000000000000ull : ~k));
+}
+constexpr uint64_t kFirstKey64 = 0x0010000000000000ull;  // below: -inf, or no value
+
+// The warp's largest key (0 = none) and the lowest lane that holds it.
+__device__ __forceinline__ uint64_t warp_best64(uint64_t k, int& src) {
+  const uint32_t hi = static_cast<uint32_t>(k >> 32);
+  const uint32_t mh = __reduce_max_sync(kFull, hi);
+  const uint32_t lo = hi == mh ? static_cast<uint32_t>(k) : 0;
+  const uint32_t ml = __reduce_max_sync(kFull, lo);
+  src = __ffs(__ballot_sync(kFull, hi == mh && static_cast<uint32_t>(k) == ml)) - 1;
+  return static_cast<uint64_t>(mh) << 32 | ml;
+}
+
+// Two largest of a set, held as (a >= b).
+__device__ __forceinline__ void push2(uint64_t& a, uint64_t& b, uint64_t v) {
+  b = max(b, min(a, v));
+  a = max(a, v);
+}
+
+// Bits of the leaders of the groups that stay (see kept_groups).
 template <int VPL>
-__device__ __forceinline__ float pick_reg(const float (&a)[VPL], int j) {
-  float v = a[0];
-#pragma unroll
-  for (int i = 1; i < VPL; ++i)
-    if (i == j) v = a[i];
-  return v;
+__device__ __forceinline__ unsigned kept_groups_exact(const TopkParams& p, int lane, const uint64_t* key) {
+  const int G = p.n_groups;
+  const bool runs = p.lane_run > 0;
+  uint64_t a = 0, b = 0;
+#pragma unroll 1
+  for (int g = 0; g < (runs ? 1 : G); ++g) {
+    uint64_t c = 0, d = 0;
+#pragma unroll 1
+    for (int j = 0; j < VPL; ++j)
+      if (runs || (lane * VPL + j) / p.group_size == g) push2(c, d, key[j]);
+#pragma unroll 1
+    for (int o = 1; o < (runs ? p.lane_run : 32); o <<= 1) {
+      const uint64_t c2 = __shfl_xor_sync(kFull, c, o), d2 = __shfl_xor_sync(kFull, d, o);
+      push2(c, d, c2);
+      push2(c, d, d2);
+    }
+    if (runs || lane == g) {
+      a = c;
+      b = d;
+    }
+  }
+  const bool leader = runs ? (lane & (p.lane_run - 1)) == 0 && lane < G * p.lane_run : lane < G;
+  double mine = -INFINITY;
+  if (a >= kFirstKey64) {
+    mine = key_value64(a);
+    if (p.rule == MOE_GROUP_TOP2_SUM && b >= kFirstKey64) mine += key_value64(b);
+  }
+  uint64_t left = leader ? order_key64(mine) + 1 : 0;  // an empty group is above no group
+  unsigned kept = 0;
+#pragma unroll 1
+  for (int i = 0; i < p.topk_groups; ++i) {
+    int src;
+    warp_best64(left, src);
+    kept |= 1u << src;
+    if (lane == src) left = 0;
+  }
+  return kept;
+}
+
+template <int VPL>
+__device__ __forceinline__ int take_k_exact(uint64_t* key, int k, int lane) {
+  int pick = -1;
+#pragma unroll 1
+  for (int i = 0; i < k; ++i) {
+    uint64_t best = 0;
+    int at = 0;
+#pragma unroll 1
+    for (int j = 0; j < VPL; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = j;
+      }
+    int src;
+    if (warp_best64(best, src) < kFirstKey64) break;
+    const int e = __shfl_sync(kFull, lane * VPL + at, src);
+    if (lane == i) pick = e;
+    if (lane == src) key[at] = 0;
+  }
+  return pick;
 }
 
 // ---- common path: 32-bit keys ------------------------------------------------
@@ -228,13 +352,61 @@ __device__ constexpr float key_slack() {
   return 1.2e-7f * VPL + 1.2e-7f;
 }
 
+// The same from 64-bit values, for groups that are runs of lanes with sorted keys: every
+// lane scores those of its experts again that may be one of the group's two largest (a, b:
+// the group's two largest keys), one after the other.
+template <bool BF16, int VPL>
+__device__ __noinline__ unsigned settle_groups(const TopkParams& p, int64_t t, int lane, const uint32_t (&key)[VPL],
+                                               bool by_score, float err, uint32_t a, uint32_t b) {
+  const bool sum = p.rule == MOE_GROUP_TOP2_SUM;
+  const uint32_t least = sum ? b : a;
+  float limit = -INFINITY;
+  if (least >= kFirstKey) {
+    const float v = bare_value<VPL>(least);
+    limit = v - 2.0f * err - 3.0f * key_slack<VPL>() * fabsf(v);
+  }
+  const ExactRow row = by_score ? exact_row<BF16, VPL>(p, t, lane) : ExactRow{};
+  uint64_t c = 0, d = 0;
+  for (int j = 0; j < VPL; ++j) {
+    uint32_t k = kNoKey;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (i == j) k = key[i];
+    const bool look = k >= kFirstKey && bare_value<VPL>(k) >= limit;
+    if (!__any_sync(kFull, look)) break;
+    if (look) {
+      const double v = exact_value<BF16>(p, t, lane * VPL + VPL - 1 - static_cast<int>(k & (VPL - 1)), by_score, row);
+      push2(c, d, order_key64(v));
+    }
+    __syncwarp();
+  }
+  for (int o = 1; o < p.lane_run; o <<= 1) {
+    const uint64_t c2 = __shfl_xor_sync(kFull, c, o), d2 = __shfl_xor_sync(kFull, d, o);
+    push2(c, d, c2);
+    push2(c, d, d2);
+  }
+  double mine = -INFINITY;
+  if (c >= kFirstKey64) mine = key_value64(c) + (sum && d >= kFirstKey64 ? key_value64(d) : 0.0);
+  const bool leader = (lane & (p.lane_run - 1)) == 0 && lane < p.n_groups * p.lane_run;
+  uint64_t left = leader ? order_key64(mine) + 1 : 0;
+  unsigned kept = 0;
+  for (int i = 0; i < p.topk_groups; ++i) {
+    int src;
+    warp_best64(left, src);
+    kept |= 1u << src;
+    if (lane == src) left = 0;
+  }
+  return kept;
+}
+
 // Bits of the leaders of the groups that stay (lane g for group g, or the first lane of
 // its run where groups are whole runs of lanes), from the keys the groups go by.
-// `undecided` is set when two groups on either side of the limit are closer than
-// their errors.
-template <int VPL>
-__device__ __forceinline__ unsigned kept_groups(const TopkParams& p, int lane, const uint32_t (&key)[VPL],
-                                                float err, bool& undecided) {
+// Where two groups on either side of the limit are closer than their errors, the groups
+// are valued again in 64 bits; `undecided` is set when that takes more than the sorted
+// keys of whole lanes.
+template <bool BF16, int VPL>
+__device__ __forceinline__ unsigned kept_groups(const TopkParams& p, int64_t t, int lane, const uint32_t (&key)[VPL],
+                                                bool by_score, float err, bool& undecided) {
   constexpr bool kSorted = VPL <= 8;
   const int gs = p.group_size, G = p.n_groups;
   const bool sum = p.rule == MOE_GROUP_TOP2_SUM;
@@ -300,30 +472,62 @@ __device__ __forceinline__ unsigned kept_groups(const TopkParams& p, int lane, c
     const float low = __shfl_sync(kFull, mine, src), high = __shfl_sync(kFull, mine, next);
     const float sizes = __shfl_sync(kFull, size, src) + __shfl_sync(kFull, size, next);
     // an empty group is exact
-    if (high != -INFINITY && !(low - high > 4.0f * err + key_slack<VPL>() * sizes)) undecided = true;
+    if (high != -INFINITY && !(low - high > 4.0f * err + key_slack<VPL>() * sizes)) {
+      if (!kSorted || p.lane_run == 0 || !(sizes < INFINITY)) undecided = true;
+      else kept = settle_groups<BF16, VPL>(p, t, lane, key, by_score, err, a, b);
+    }
   }
   return kept;
 }
 
+// The m choices that lanes 0 .. m-1 hold (in `pick`), put in the order of their 64-bit
+// values: lane i ends with the i-th.
+template <bool BF16, int VPL>
+__device__ __noinline__ int settle_order(const TopkParams& p, int64_t t, int lane, int pick, int m, bool by_score) {
+  const ExactRow row = by_score ? exact_row<BF16, VPL>(p, t, lane) : ExactRow{};
+  double v = 0.0;
+  if (lane < m) v = exact_value<BF16>(p, t, pick, by_score, row);
+  __syncwarp();
+  int place = 0, sorted = -1;
+  for (int i = 0; i < m; ++i) {
+    const double o = __shfl_sync(kFull, v, i);
+    const int e = __shfl_sync(kFull, pick, i);
+    place += (o > v || (o == v && e < pick)) ? 1 : 0;
+  }
+  for (int i = 0; i < m; ++i) {
+    const int at = __shfl_sync(kFull, place, i), e = __shfl_sync(kFull, pick, i);
+    if (lane == at) sorted = e;
+  }
+  return sorted;
+}
+
 // k rounds of the warp's largest key. Lane i ends with the i-th choice in `pick` (-1:
-// none left); one more round looks at the value behind the last. `err` < 0: the
-// keys lost nothing, every comparison is exact.
-template <int VPL>
-__device__ __forceinline__ void take_k(uint32_t (&key)[VPL], int k, int lane, float err, bool& undecided, int& pick) {
+// none left). `err` < 0: the keys lost nothing, every comparison is exact. Else one or two
+// more rounds look at the values behind the last; where neighbours are closer than both may
+// be off, and the k-th or the one behind it is clear of the next, those before that gap
+// are put in the order of their 64-bit values. `undecided`: there is no such gap.
+template <bool BF16, int VPL>
+__device__ __forceinline__ void take_k(const TopkParams& p, int64_t t, uint32_t (&key)[VPL], int lane, bool by_score,
+                                       float err, bool& undecided, int& pick) {
   constexpr bool kSorted = VPL <= 8;
   constexpr uint32_t kIndex = VPL - 1;
+  const int k = p.k;
   uint32_t best = key[0], mine = kNoKey;
   if (!kSorted) {
 #pragma unroll
     for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
   }
   int from = 0;
-  const int rounds = err >= 0.0f ? min(k + 1, 32) : k;
-  for (int i = 0; i < rounds; ++i) {
+  // Two neighbours closer than both may be off (infinite values are close to everything).
+  auto near = [&](uint32_t hi, uint32_t lo) {
+    const float a = key_value(hi), b = key_value(lo);
+    return lo >= kFirstKey && !(a - b > 2.0f * err + key_slack<VPL>() * (fabsf(a) + fabsf(b)));
+  };
+  auto round = [&](int i) {
     // the values alone decide; among equal ones the lowest lane, in it the lowest register
     const uint32_t head = best | kIndex;
     const uint32_t m = __reduce_max_sync(kFull, head);
-    if (m < kFirstKey) break;
+    if (m < kFirstKey) return false;
     const int src = __ffs(__ballot_sync(kFull, head == m)) - 1;
     const uint32_t full = __shfl_sync(kFull, best, src);
     mine = lane == i ? full : mine;
@@ -342,120 +546,35 @@ __device__ __forceinline__ void take_k(uint32_t (&key)[VPL], int k, int lane, fl
         best = max(best, key[j]);
       }
     }
-  }
-  pick = lane < k && mine >= kFirstKey ? from * VPL + (VPL - 1 - static_cast<int>(mine & (VPL - 1))) : -1;
+    return true;
+  };
+  const int rounds = err >= 0.0f ? min(k + 1, 32) : k;
+  for (int i = 0; i < rounds; ++i)
+    if (!round(i)) break;
+  bool has = mine >= kFirstKey;
   if (err >= 0.0f) {
-    // neighbours closer than both may be off: the fp32 error and the index bits
-    const uint32_t next = __shfl_down_sync(kFull, mine, 1);
-    const float a = key_value(mine), b = key_value(next);
-    const float e = 2.0f * err + key_slack<VPL>() * (fabsf(a) + fabsf(b));
-    const bool close = lane < 31 && next >= kFirstKey && !(a - b > e);
-    // with k = 32 there is no lane for the value behind the last: never decided here
-    if (__any_sync(kFull, close) || k == 32) undecided = true;
-  }
-}
-
-// ---- 64-bit values -------------------------------------------------------------
-// The same steps on 64-bit keys that sort like doubles. One such token can be the last
-// of its kernel, so its own time counts: 16384 tokens of 256 experts took 16 us longer
-// when every round was a shuffle reduction of doubles.
-
-__device__ __forceinline__ uint64_t order_key64(double v) {
-  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
-  return b ^ (static_cast<uint64_t>(static_cast<int64_t>(b) >> 63) | 0x8000000000000000ull);
-}
-__device__ __forceinline__ double key_value64(uint64_t k) {
-  return __longlong_as_double(
-      static_cast<long long>(k & 0x8000000000000000ull ? k ^ 0x8000000000000000ull : ~k));
-}
-constexpr uint64_t kFirstKey64 = 0x0010000000000000ull;  // below: -inf, or no value
-
-// The warp's largest key (0 = none) and the lowest lane that holds it.
-__device__ __forceinline__ uint64_t warp_best64(uint64_t k, int& src) {
-  const uint32_t hi = static_cast<uint32_t>(k >> 32);
-  const uint32_t mh = __reduce_max_sync(kFull, hi);
-  const uint32_t lo = hi == mh ? static_cast<uint32_t>(k) : 0;
-  const uint32_t ml = __reduce_max_sync(kFull, lo);
-  src = __ffs(__ballot_sync(kFull, hi == mh && static_cast<uint32_t>(k) == ml)) - 1;
-  return static_cast<uint64_t>(mh) << 32 | ml;
-}
-
-// Two largest of a set, held as (a >= b).
-__device__ __forceinline__ void push2(uint64_t& a, uint64_t& b, uint64_t v) {
-  b = max(b, min(a, v));
-  a = max(a, v);
-}
-
-// Bits of the leaders of the groups that stay (see kept_groups).
-template <int VPL>
-__device__ __forceinline__ unsigned kept_groups_exact(const TopkParams& p, int lane, const uint64_t (&key)[VPL]) {
-  const int G = p.n_groups;
-  uint64_t a = 0, b = 0;
-  bool leader = lane < G;
-  if (p.lane_run > 0) {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) push2(a, b, key[j]);
-    for (int o = 1; o < p.lane_run; o <<= 1) {
-      const uint64_t c = __shfl_xor_sync(kFull, a, o), d = __shfl_xor_sync(kFull, b, o);
-      push2(a, b, c);
-      push2(a, b, d);
-    }
-    leader = (lane & (p.lane_run - 1)) == 0 && lane < G * p.lane_run;
-  } else {
-    for (int g = 0; g < G; ++g) {
-      uint64_t c = 0, d = 0;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if ((lane * VPL + j) / p.group_size == g) push2(c, d, key[j]);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t c2 = __shfl_xor_sync(kFull, c, o), d2 = __shfl_xor_sync(kFull, d, o);
-        push2(c, d, c2);
-        push2(c, d, d2);
+    // lanes whose value is near the next lane's (lane 31 knows no next)
+    auto close = [&] {
+      const uint32_t next = __shfl_down_sync(kFull, mine, 1);
+      return __ballot_sync(kFull, has && (lane == 31 || near(mine, next)));
+    };
+    unsigned near_next = close();
+    if (near_next & (k == 32 ? kFull : (1u << k) - 1u)) {  // among the choices, or behind the last
+      int m = k;
+      if ((near_next >> (k - 1)) & 1u) {  // is the one behind the last clear of the next?
+        if (k < 31) round(k + 1);
+        has = mine >= kFirstKey;
+        near_next = close();
+        m = k < 31 && !((near_next >> k) & 1u) ? k + 1 : 0;
       }
-      if (lane == g) {
-        a = c;
-        b = d;
-      }
+      pick = has ? from * VPL + (VPL - 1 - static_cast<int>(mine & kIndex)) : -1;
+      if (m == 0 || __any_sync(kFull, has && !(fabsf(key_value(mine)) < INFINITY))) undecided = true;
+      else pick = settle_order<BF16, VPL>(p, t, lane, pick, min(m, __popc(__ballot_sync(kFull, has))), by_score);
+      if (lane >= k) pick = -1;
+      return;
     }
   }
-  double mine = -INFINITY;
-  if (a >= kFirstKey64) {
-    mine = key_value64(a);
-    if (p.rule == MOE_GROUP_TOP2_SUM && b >= kFirstKey64) mine += key_value64(b);
-  }
-  uint64_t left = leader ? order_key64(mine) + 1 : 0;  // an empty group is above no group
-  unsigned kept = 0;
-  for (int i = 0; i < p.topk_groups; ++i) {
-    int src;
-    warp_best64(left, src);
-    kept |= 1u << src;
-    if (lane == src) left = 0;
-  }
-  return kept;
-}
-
-template <int VPL>
-__device__ __forceinline__ int take_k_exact(uint64_t (&key)[VPL], int k, int lane) {
-  int pick = -1;
-  for (int i = 0; i < k; ++i) {
-    uint64_t best = key[0];
-    int at = 0;
-#pragma unroll
-    for (int j = 1; j < VPL; ++j)
-      if (key[j] > best) {
-        best = key[j];
-        at = j;
-      }
-    int src;
-    if (warp_best64(best, src) < kFirstKey64) break;
-    const int e = __shfl_sync(kFull, lane * VPL + at, src);
-    if (lane == i) pick = e;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (lane == src && j == at) key[j] = 0;
-  }
-  return pick;
+  pick = has && lane < k ? from * VPL + (VPL - 1 - static_cast<int>(mine & kIndex)) : -1;
 }
 
 // Scores of this lane's experts, the row's largest logit and, for softmax, the sum.
@@ -529,46 +648,28 @@ __device__ __forceinline__ float score_error(int score, float s_top) {
 template <bool BF16, int VPL>
 __device__ __noinline__ int choose_exact(const TopkParams& p, int64_t t, int lane) {
   const bool biased = p.bias != nullptr, sums = p.n_groups > 1 && p.rule == MOE_GROUP_TOP2_SUM;
-  float l[VPL];
-  load_row<BF16, VPL>(p.logits, t, p.E, lane, l);
+  const ExactRow row = biased || sums ? exact_row<BF16, VPL>(p, t, lane) : ExactRow{};
   uint64_t key[VPL];
-  auto by_logit = [&] {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = order_key64(static_cast<double>(l[j]));
-  };
-  auto by_score = [&] {
-    double top = 0.0, z = 1.0;
-    if (p.score == MOE_SCORE_SOFTMAX) {
-      float m = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) m = fmaxf(m, l[j]);
-      m = key_value(__reduce_max_sync(kFull, order_key(m)));
-      top = m > -INFINITY ? static_cast<double>(m) : 0.0;
-      z = 0.0;
+  unsigned kept = kFull;
 #pragma unroll 1
-      for (int j = 0; j < VPL; ++j) z += exp(static_cast<double>(pick_reg<VPL>(l, j)) - top);
-      z = warp_add(z);
-    }
+  for (int pass = 0; pass < 2; ++pass) {  // sums without a bias: groups by scores, then experts by logits
+    const bool by_score = biased || (pass == 0 && sums);
 #pragma unroll 1
     for (int j = 0; j < VPL; ++j) {
-      const float x = pick_reg<VPL>(l, j);
       const int e = lane * VPL + j;
-      double v = p.score == MOE_SCORE_SOFTMAX ? exp(static_cast<double>(x) - top) / z
-                                              : 1.0 / (1.0 + exp(-static_cast<double>(x)));
-      if (biased && e < p.E) v += static_cast<double>(__ldg(p.bias + e));
-      const uint64_t k = x == -INFINITY || v != v ? 0 : order_key64(v);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i == j) key[i] = k;
+      uint64_t k = 0;
+      if (e < p.E && load_logit<BF16>(p.logits, t * p.E + e) > -INFINITY) {
+        const double v = exact_value<BF16>(p, t, e, by_score, row);
+        if (!(v != v)) k = order_key64(v);
+      }
+      key[j] = k;
+      __syncwarp();
     }
-  };
-  if (biased || sums) by_score();
-  else by_logit();
-  unsigned kept = kFull;
-  if (p.n_groups > 1) kept = kept_groups_exact<VPL>(p, lane, key);
-  if (sums && !biased) by_logit();
+    if (pass == 0 && p.n_groups > 1) kept = kept_groups_exact<VPL>(p, lane, key);
+    if (biased || !sums) break;
+  }
   if (p.n_groups > 1) {
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < VPL; ++j) {
       const int g = p.lane_run > 0 ? lane & ~(p.lane_run - 1) : (lane * VPL + j) / p.group_size;
       if (g >= 32 || !((kept >> g) & 1u)) key[j] = 0;
@@ -630,7 +731,7 @@ __device__ __forceinline__ int choose(const TopkParams& p, int64_t t, int lane, 
   float err = score_error(p.score, s_top);
   if (sums && !biased) {
     by_score();
-    kept = kept_groups<VPL>(p, lane, key, err, undecided);
+    kept = kept_groups<BF16, VPL>(p, t, lane, key, true, err, undecided);
   }
   if (biased) {
     by_score();
@@ -645,7 +746,7 @@ __device__ __forceinline__ int choose(const TopkParams& p, int64_t t, int lane, 
     // exact where no logit has a bit that the index took
     err = VPL > 1 && __any_sync(kFull, (lost & (VPL - 1)) != 0) ? 0.0f : -1.0f;
   }
-  if (groups && !(sums && !biased)) kept = kept_groups<VPL>(p, lane, key, err, undecided);
+  if (groups && !(sums && !biased)) kept = kept_groups<BF16, VPL>(p, t, lane, key, biased, err, undecided);
   if (groups && p.lane_run > 0) {
     if (!((kept >> (lane & ~(p.lane_run - 1))) & 1u)) {
 #pragma unroll
@@ -661,7 +762,7 @@ __device__ __forceinline__ int choose(const TopkParams& p, int64_t t, int lane, 
     if (VPL > 1 && VPL <= 8) sort_keys<VPL>(key);  // holes inside a lane
   }
   int pick;
-  take_k<VPL>(key, p.k, lane, err, undecided, pick);
+  take_k<BF16, VPL>(p, t, key, lane, biased, err, undecided, pick);
   if (undecided) pick = choose_exact<BF16, VPL>(p, t, lane);  // the same on every lane
   return pick;
 }

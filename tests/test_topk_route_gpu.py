@@ -374,3 +374,34 @@ def test_route_on_other_streams_and_in_graphs():
         torch.cuda.synchronize()
         check(r, static, 8, "sigmoid", bias, 8, 4, "top2", True, 1.0, n)
         assert (back[n:] == 0).all() and bool(torch.isfinite(back).all())
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,keep", [(64, 5, 1, 1), (256, 8, 1, 1), (256, 8, 8, 4), (40, 31, 1, 1), (33, 32, 1, 1),
+                                             (96, 7, 3, 2), (512, 6, 16, 5)])
+def test_route_single_near_ties(kind, E, k, groups, keep):
+    """Values 0.01 apart but for one pair (or three, or a pair of groups) that fp32 cannot order."""
+    g = gen(E + k)
+    row = torch.randn(E, generator=g, device=DEV)
+    _, _, s = ref.scores(row.double().cpu().numpy()[None], kind)
+    order = torch.randperm(E, generator=g, device=DEV).cpu().numpy()
+    for at in range(0, k + 3):
+        for width in (2, 3):
+            c = np.empty(E)
+            c[order] = 5.0 - 0.01 * np.arange(E)
+            if at + width <= E:
+                c[order[at:at + width]] = c[order[at]]
+            if groups > 1 and at % 2:
+                # two groups of the same largest pair of values
+                gs = E // groups
+                a, b = (order[at] // gs) * gs, (order[(at + 9) % E] // gs) * gs
+                c[b:b + 2] = np.sort(c[a:a + gs])[::-1][:2]
+            bias = torch.from_numpy((c - s[0]).astype(np.float32)).to(DEV)
+            for rule in ("max", "top2") if groups > 1 else ("max",):
+                run_and_check(row[None].contiguous(), k, kind, bias=bias, groups=groups, keep=keep, rule=rule)
+            # the same for logits alone, one step of fp32 apart
+            l = torch.from_numpy(np.round(c * 2 ** 20).astype(np.float32) / 2 ** 20).to(DEV)
+            if at + width <= E:
+                e = torch.tensor(order[at:at + width], device=DEV)
+                l[e] += torch.arange(width, device=DEV) * 2.0 ** -21
+            run_and_check(l[None].contiguous(), k, kind, groups=groups, keep=keep, rule="max")
