@@ -1081,11 +1081,22 @@ __global__ void __launch_bounds__(256, 1)
 // epilogue of one tile runs beside the next one's products). Tiles are handed out in
 // order from a counter, row tiles of one weight tile next to one another, so that the
 // pairs that run together share weights in L2 (tile_order.cuh).
+//
+// With 256-row tiles the operands a CTA loads for 512 tensor cycles, 64 B a cycle, are
+// more than L2 delivers (about 50): the tensor pipe was busy 72 % of the cycles. Tiles of
+// 512 rows (H = 2) use each weight stage for two MMAs, 48 KB for 1024 cycles. Their two
+// halves are the two accumulators, so the next tile cannot start beside this one's
+// epilogue; it starts on the first half as soon as that is in registers, and runs ahead
+// on it by up to the ring's stages while the second is fetched.
 
-constexpr int PAIR_ROWS = 256;
-constexpr int PX_BYTES = 128 * BK;              // 16 KB: this CTA's 128 rows
-constexpr int PSTAGE_BYTES = PX_BYTES + WBOX;   // 32 KB
-constexpr int PSTAGES = 6;
+constexpr int PAIR_ROWS = 256;                  // rows of one MMA
+constexpr int PX_BYTES = 128 * BK;              // 16 KB: this CTA's 128 rows of it
+template <int H>
+struct PairCfg {
+  static constexpr int ROWS = H * PAIR_ROWS;               // of a tile
+  static constexpr int STAGE_BYTES = H * PX_BYTES + WBOX;  // 32 or 48 KB
+  static constexpr int STAGES = H == 1 ? 6 : 4;
+};
 constexpr int PQ = 4;             // tile-id queue: the producer leads by at most 3 tiles
 // Epilogue warps: sets of four (one per 32 TMEM lanes), each set with its own columns.
 constexpr int PSETS = 4;
@@ -1093,23 +1104,28 @@ constexpr int PEPI = 4 * PSETS;
 constexpr int PTHREADS = 128 + 32 * PEPI;
 constexpr int PQ_READERS = 2 + 2 * PEPI;  // odd producer, MMA thread, the epilogue warps of both CTAs
 constexpr int PSCALES = 2 * 128 / PSETS;  // channel scales an epilogue warp keeps in shared memory
-constexpr int PSMEM = PSTAGES * PSTAGE_BYTES + 1024 + 256 + PEPI * PSCALES * 4 + 2 * (kMaxExperts + 1) * 4;
+constexpr int PSMEM = 6 * 32 * 1024 + 1024 + 256 + PEPI * PSCALES * 4 + 2 * (kMaxExperts + 1) * 4;
 static_assert(PSMEM <= 232448, "shared memory above the per-block limit");
-static_assert((2 * PSTAGES + 4 + 2 * PQ + 1) * 8 + 8 + 4 * PQ <= 256, "barrier area too small");
+static_assert(PairCfg<1>::STAGES * PairCfg<1>::STAGE_BYTES <= 6 * 32 * 1024 &&
+                  PairCfg<2>::STAGES * PairCfg<2>::STAGE_BYTES <= 6 * 32 * 1024,
+              "ring larger than its share");
+static_assert((2 * PairCfg<1>::STAGES + 4 + 2 * PQ + 1) * 8 + 8 + 4 * PQ <= 256, "barrier area too small");
 
-// Bounded wait with cluster-scope acquire (for barriers that the other CTA arrives on).
+// Waits with cluster-scope acquire (for barriers that the other CTA arrives on): one look,
+// and bounded.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
-  auto once = [&]() {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-  };
+  auto once = [&]() { return mbar_try_wait_cluster(bar, parity); };
   if (once()) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
@@ -1184,10 +1200,11 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-template <bool DUAL, bool OB>
+template <int H, bool DUAL, bool OB>
 __global__ void __launch_bounds__(PTHREADS, 1)
     moe_int8_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
                          const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ Params p) {
+  constexpr int PSTAGES = PairCfg<H>::STAGES, PSTAGE_BYTES = PairCfg<H>::STAGE_BYTES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + PSTAGES * PSTAGE_BYTES);
@@ -1249,8 +1266,8 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     const int mt = pre[t.e + 1] - pre[t.e];
     int m, c, ks;
     tile_coords(tile - pre[t.e] * p.nt, mt, p.nt, group_for(mt, p.group_rows, p.group_limit), m, c, ks);
-    t.row0 = off[t.e] + m * PAIR_ROWS;
-    t.rows = min(PAIR_ROWS, off[t.e + 1] - t.row0);
+    t.row0 = off[t.e] + m * PairCfg<H>::ROWS;
+    t.rows = min(PairCfg<H>::ROWS, off[t.e + 1] - t.row0);
     t.n0 = c * (DUAL ? 128 : 256);
     return t;
   };
@@ -1299,6 +1316,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       if (tile < 0) break;
       const Tile t = decode(tile);
       const int row = t.row0 + 128 * static_cast<int>(rank);
+      const int nh = H == 2 && t.rows > PAIR_ROWS ? 2 : 1;  // halves with rows
       // gated pair: the even CTA holds the gate columns, the odd one the up columns
       const CUtensorMap* wmap = DUAL && rank == 1 ? &tm_w1 : &tm_w0;
       const int n = DUAL ? t.n0 : t.n0 + 128 * static_cast<int>(rank);
@@ -1309,9 +1327,10 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         }
         uint8_t* xs = smem + stage * PSTAGE_BYTES;
         const uint32_t bar0 = mapa_shared(&full_bar[stage], 0);
-        if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * PSTAGE_BYTES);
+        if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * (nh * PX_BYTES + WBOX));
+        tma_load_3d_pair(xs + H * PX_BYTES, wmap, bar0, n, kb * BK, t.e);
         tma_load_2d_pair(xs, &tm_x, bar0, kb * BK, row);
-        tma_load_3d_pair(xs + PX_BYTES, wmap, bar0, n, kb * BK, t.e);
+        if (H == 2 && nh == 2) tma_load_2d_pair(xs + PX_BYTES, &tm_x, bar0, kb * BK, row + PAIR_ROWS);
         if (++stage == PSTAGES) {
           stage = 0;
           phase ^= 1;
@@ -1344,30 +1363,85 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       const int tile = q_take(i);
       if (tile == -2) ok = false;
       if (tile < 0) break;
+      // Accumulators take turns, one per half of a tile.
+      const int a0 = acc, nh = H == 2 && decode(tile).rows > PAIR_ROWS ? 2 : 1;
       if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1) || *abort_flag) ok = false;
       tc_fence_after();
-      const uint32_t d = tmem_base + acc * 256;
-      for (int kb = 0; ok && kb < p.kb; ++kb) {
-        if (!mbar_wait(&full_bar[stage], phase, kWaitLimitNs) || *abort_flag) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t xs = smem_u32(smem + stage * PSTAGE_BYTES), ws = xs + PX_BYTES;
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+      auto issue = [&](int st, int half, int a, bool first) {
+        const uint32_t xs = smem_u32(smem + st * PSTAGE_BYTES), ws = xs + H * PX_BYTES;
 #pragma unroll
         for (int k = 0; k < BK / 32; ++k)
-          umma_s8_pair(d, smem_desc_sw128(xs + k * 32, 16, 1024), smem_desc_sw128(ws + k * 4096, WBOX, 1024), idesc,
-                       kb > 0 || k > 0);
+          umma_s8_pair(tmem_base + a * 256, smem_desc_sw128(xs + half * PX_BYTES + k * 32, 16, 1024),
+                       smem_desc_sw128(ws + k * 4096, WBOX, 1024), idesc, !first || k > 0);
+      };
+      auto release = [&] {
         umma_commit_pair(&empty_bar[stage], 0x3);
         if (++stage == PSTAGES) {
           stage = 0;
           phase ^= 1;
         }
-      }
-      if (ok) umma_commit_pair(&tfull_bar[acc], 0x3);
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1;
+      };
+      if (nh == 1) {
+        for (int kb = 0; ok && kb < p.kb; ++kb) {
+          if (!mbar_wait(&full_bar[stage], phase, kWaitLimitNs) || *abort_flag) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          issue(stage, 0, a0, kb == 0);
+          release();
+        }
+        if (ok) umma_commit_pair(&tfull_bar[a0], 0x3);
+      } else if constexpr (H == 2) {
+        const int a1 = acc;
+        const uint32_t p1 = acc_phase ^ 1;
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+        // k0, k1: K blocks issued to the first and the second half; (s0, ph0) is the
+        // first half's place in the ring, (stage, phase) the second's.
+        bool ready = false;
+        int k0 = 0, k1 = 0, s0 = stage;
+        uint32_t ph0 = phase;
+        auto issue0 = [&] {
+          if (!mbar_wait(&full_bar[s0], ph0, kWaitLimitNs) || *abort_flag) return false;
+          tc_fence_after();
+          issue(s0, 0, a0, k0 == 0);
+          if (++s0 == PSTAGES) {
+            s0 = 0;
+            ph0 ^= 1;
+          }
+          if (++k0 == p.kb) umma_commit_pair(&tfull_bar[a0], 0x3);
+          return true;
+        };
+        while (ok && k1 < p.kb) {
+          if (!ready) {
+            ready = mbar_try_wait_cluster(&tempty_bar[a1], p1);
+            if (!ready && k0 < p.kb && k0 - k1 < PSTAGES) {
+              ok = issue0();
+              continue;
+            }
+            if (!ready && (!mbar_wait_cluster(&tempty_bar[a1], p1) || *abort_flag)) {
+              ok = false;
+              break;
+            }
+            ready = true;
+            tc_fence_after();
+          }
+          if (k0 == k1 && !issue0()) {
+            ok = false;
+            break;
+          }
+          issue(stage, 1, a1, k1 == 0);
+          release();
+          ++k1;
+        }
+        if (ok) umma_commit_pair(&tfull_bar[a1], 0x3);
       }
     }
     if (!ok) {
@@ -1388,39 +1462,51 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       const int tile = q_take_warp(i);
       if (tile == -1) break;
       Tile t{};
-      int64_t row = 0;
-      bool valid = false;
-      float a = 0.0f, ag = 0.0f;
+      int nh = 1;
+      float a[H], ag[H];
+      const int r0 = 128 * static_cast<int>(rank) + 32 * q + lane;  // row of the tile, and of its second half + 256
       if (tile >= 0) {  // what the tile needs besides its sums, on its way before they are
         t = decode(tile);
-        const int r = 128 * static_cast<int>(rank) + 32 * q + lane;
-        row = static_cast<int64_t>(t.row0) + r;
-        valid = r < t.rows;
-        if (valid) {
-          a = __ldg(p.a + row);
-          ag = p.gate != nullptr ? a * __ldg(p.gate + row) : a;
+        if (H == 2 && t.rows > PAIR_ROWS) nh = 2;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const int r = r0 + h * PAIR_ROWS;
+          const int64_t row = static_cast<int64_t>(t.row0) + r;
+          a[h] = r < t.rows ? __ldg(p.a + row) : 0.0f;
+          ag[h] = r < t.rows && p.gate != nullptr ? a[h] * __ldg(p.gate + row) : a[h];
         }
         pair_scales<DUAL>(p, t.e, t.n0, c0, lane, sc);
       }
-      if (tile == -2 || !warp_wait(&tfull_bar[acc], acc_phase, abort_flag)) {
+      bool ok = tile != -2;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        if (!ok || h >= nh) break;
+        if (!warp_wait(&tfull_bar[acc], acc_phase, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // The sums go to registers at once, so that the accumulator is free for the next
+        // tile before this one is scaled and stored.
+        const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * 256 + c0;
+        uint32_t u[32], v[32];
+        tmem_ld32x2(tb, tb + (DUAL ? 128 : 32), u, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty0[acc]);
+        const int r = r0 + h * PAIR_ROWS;
+        if (r < t.rows)
+          pair_epilogue<DUAL, OB>(p, t.n0 + c0, u, v, sc, static_cast<int64_t>(t.row0) + r, a[h], ag[h]);
+        __syncwarp();  // every lane has read the scales
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+      if (!ok) {
         atomicOr(p.status, kStatusEpilogueTimeout);
         *abort_flag = 1;
         break;
-      }
-      tc_fence_after();
-      // The sums go to registers at once, so that the accumulator is free for the next
-      // tile but one before this one is scaled and stored.
-      const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * 256 + c0;
-      uint32_t u[32], v[32];
-      tmem_ld32x2(tb, tb + (DUAL ? 128 : 32), u, v);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(tempty0[acc]);
-      if (valid) pair_epilogue<DUAL, OB>(p, t.n0 + c0, u, v, sc, row, a, ag);
-      __syncwarp();  // every lane has read the scales
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1;
       }
     }
   }
@@ -1466,7 +1552,8 @@ Layout plan(int64_t R, int64_t K, int64_t N, int32_t n_experts, moe_dtype_t x_dt
     if (L.split == 0 && tiles <= s[1] && kb >= 2 * s[0]) L.split = s[0];
   if (L.split > 0 && tiles * L.split < 96 && kb > 24 * L.split && R <= 128 * static_cast<int64_t>(n_experts))
     L.split = 0;
-  if (L.split == 0 && R > 128 * static_cast<int64_t>(n_experts)) L.tile_rows = PAIR_ROWS;
+  if (L.split == 0 && R > 128 * static_cast<int64_t>(n_experts))
+    L.tile_rows = R >= 512 * static_cast<int64_t>(n_experts) ? 2 * PAIR_ROWS : PAIR_ROWS;
   L.status = take(256);
   L.sched = take(sizeof(Sched));
   L.counters = take(sizeof(int32_t) * kMaxCtas);
@@ -1533,13 +1620,13 @@ cudaError_t launch_stream(const moe_int8_args_t* a, const void* q, Params p, int
   return launch_kernel(kern, grid, 256, kSmem, s, 1, false, tx, tw0, tw1, p);
 }
 
-template <bool DUAL, bool OB>
+template <int H, bool DUAL, bool OB>
 cudaError_t launch_pair(const moe_int8_args_t* a, const void* q, Params p, cudaStream_t s) {
-  auto kern = moe_int8_pair_kernel<DUAL, OB>;
+  auto kern = moe_int8_pair_kernel<H, DUAL, OB>;
   const cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), PSMEM);
   if (err != cudaSuccess) return err;
   // Clusters of two that fit at once on this device (queried once per device).
-  const int max_pairs = once_per_device(reinterpret_cast<const void*>(&launch_pair<DUAL, OB>), [](const void*) {
+  const int max_pairs = once_per_device(reinterpret_cast<const void*>(&launch_pair<H, DUAL, OB>), [](const void*) {
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = 2;
@@ -1552,7 +1639,7 @@ cudaError_t launch_pair(const moe_int8_args_t* a, const void* q, Params p, cudaS
     c.attrs = &at;
     c.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, moe_int8_pair_kernel<DUAL, OB>, &c) != cudaSuccess || n <= 0)
+    if (cudaOccupancyMaxActiveClusters(&n, moe_int8_pair_kernel<H, DUAL, OB>, &c) != cudaSuccess || n <= 0)
       n = device_sm_count() / 2;
     return n;
   });
@@ -1560,9 +1647,10 @@ cudaError_t launch_pair(const moe_int8_args_t* a, const void* q, Params p, cudaS
   if (!row_map(&tx, q, a, 128) || !weight_map(&tw0, a->w, a) || !weight_map(&tw1, DUAL ? a->w_up : a->w, a))
     return cudaErrorInvalidValue;
   p.nt = static_cast<int32_t>((a->N + (DUAL ? 127 : 255)) / (DUAL ? 128 : 256));
-  p.group_rows = row_group_size(PAIR_ROWS, (a->K + 1) / 2, tc::kL2GroupBytes);
-  p.group_limit = row_group_size(PAIR_ROWS, (a->K + 1) / 2, tc::kL2UngroupedBytes);
-  const int64_t most = ((a->R + PAIR_ROWS - 1) / PAIR_ROWS + a->n_experts) * p.nt;
+  constexpr int ROWS = PairCfg<H>::ROWS;
+  p.group_rows = row_group_size(ROWS, (a->K + 1) / 2, tc::kL2GroupBytes);
+  p.group_limit = row_group_size(ROWS, (a->K + 1) / 2, tc::kL2UngroupedBytes);
+  const int64_t most = ((a->R + ROWS - 1) / ROWS + a->n_experts) * p.nt;
   return launch_kernel(kern, 2 * static_cast<unsigned>(std::min<int64_t>(most, max_pairs)), PTHREADS, PSMEM, s, 2, false,
                        tx, tw0, tw1, p);
 }
@@ -1679,11 +1767,16 @@ moe_status_t moe_int8_product(const moe_int8_args_t* a, void* workspace, size_t 
     return ob ? i8::launch_stream<ROWS, false, true>(a, q, p, L.split, prepared, s)
               : i8::launch_stream<ROWS, false, false>(a, q, p, L.split, prepared, s);
   };
+  auto pair = [&](auto h) {
+    constexpr int H = decltype(h)::value;
+    if (dual) return ob ? i8::launch_pair<H, true, true>(a, q, p, s) : i8::launch_pair<H, true, false>(a, q, p, s);
+    return ob ? i8::launch_pair<H, false, true>(a, q, p, s) : i8::launch_pair<H, false, false>(a, q, p, s);
+  };
   cudaError_t e;
   if (L.tile_rows == 64) e = form(std::integral_constant<int, 64>{});
   else if (L.tile_rows == 128) e = form(std::integral_constant<int, 128>{});
-  else if (dual) e = ob ? i8::launch_pair<true, true>(a, q, p, s) : i8::launch_pair<true, false>(a, q, p, s);
-  else e = ob ? i8::launch_pair<false, true>(a, q, p, s) : i8::launch_pair<false, false>(a, q, p, s);
+  else if (L.tile_rows == 256) e = pair(std::integral_constant<int, 1>{});
+  else e = pair(std::integral_constant<int, 2>{});
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -111,7 +111,8 @@ def check(c, got, act="gelu", tail=None):
 @pytest.mark.parametrize("R,K,N,rows", [
     (1, 16, 16, None), (1, 2048, 512, None), (3, 144, 272, [2, 1]), (17, 128, 128, [0, 17, 0]), (64, 256, 512, [8] * 8),
     (65, 6144, 144, [1, 63, 1]), (129, 1040, 2064, None), (333, 512, 400, None), (200, 4096, 1040, [100, 0, 30, 70, 0]),
-    (700, 640, 272, [10, 450, 0, 240])])
+    (700, 640, 272, [10, 450, 0, 240]), (700, 640, 4112, [10, 450, 0, 240]), (1300, 640, 2064, None),
+    (1811, 272, 1552, [700, 0, 1111]), (1600, 1040, 2064, [1, 512, 1087])])
 @pytest.mark.parametrize("pair", [False, True])
 def test_sizes(R, K, N, rows, x, out, pair):
     c = make(R, K, N, len(rows) if rows else 1, R + K + N, x=x, pair=pair, rows=rows, gate=R % 2 == 1)
