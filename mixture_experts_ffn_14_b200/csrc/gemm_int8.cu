@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <type_traits>
 
@@ -1527,13 +1528,42 @@ struct Layout {
   int32_t split;      // CTAs per tile of the split form, 0: another form
 };
 
+// Row tiles of `rows` rows that R rows of n experts make: exact for one expert, else the
+// expectation for counts close to normal with mean and variance R / n.
+double row_tiles(int64_t R, int32_t n, int rows) {
+  if (n == 1) return static_cast<double>((R + rows - 1) / rows);
+  const double m = static_cast<double>(R) / n, sd = std::sqrt(m);
+  double total = 0.0, weight = 0.0;
+  for (int i = -40; i <= 40; ++i) {
+    const double z = i / 10.0, c = std::max(m + z * sd, 0.0), w = std::exp(-0.5 * z * z);
+    total += w * std::ceil(c / rows);
+    weight += w;
+  }
+  return n * total / weight;
+}
+
+// Pair form: whether tiles of 512 rows end sooner than tiles of 256. In units of one
+// 256-row tile: a full tall tile takes 1.76, one with rows in its first half alone 1.15 (a
+// shorter ring); a wave counts half of its last tile as lost, and fewer tiles than
+// pairs take one tile's time. Measured, us, 512 against 256: Grok-1 gate/up, 287, 437
+// and 1024 rows per expert 1117 and 1238, 1140 and 1248, 2184 and 2382; 256 rows 753 and
+// 712; down, 437 and 525 rows 561 and 616, 950 and 852; 571 x 8400 x 304 gated, 104 and 67.
+bool tall_tiles(int64_t R, int32_t n, int64_t nt) {
+  constexpr double kPairs = 74.0, kFull = 1.76, kHalf = 1.15;
+  const double t256 = row_tiles(R, n, 256) * nt, t512 = row_tiles(R, n, 512) * nt;
+  const double full = t256 - t512, half = t512 - full;
+  const double low = t256 <= kPairs ? 1.0 : t256 / kPairs + 0.5;
+  const double tall = t512 <= kPairs ? kFull : (full * kFull + half * kHalf) / kPairs + 0.5 * kFull;
+  return tall < low;
+}
+
 // Which form, from the sizes alone (the rows of each expert are only known on the device):
 // - split form if the tiles there can be at most leave room for two CTAs or more each (us,
 //   split against stream or pair form: 16 x 4096 x 4096 9.0 and 11.6, 64 rows 10.7 and
 //   20-25, 128 rows 13.1 and 28-39, 333 rows 18.4 and 33.8), unless few CTAs would have
 //   long runs (16 x 14336 x 4096: 28 K blocks on 64 CTAs 19.2, stream form 17.5);
 // - else by the rows an expert has on average: up to 48 the stream form in tiles of 64, up
-//   to 128 in tiles of 128, above them the pair form. Measured at the Grok-1 shape,
+//   to 128 in tiles of 128, above them the pair form in tiles of 256 or 512. Measured at the Grok-1 shape,
 //   gate/up and down, us: 128 rows per expert, stream 612 and 259, pair 698 and 339; 192,
 //   stream 1078, pair 705.
 Layout plan(int64_t R, int64_t K, int64_t N, int32_t n_experts, moe_dtype_t x_dtype, bool dual) {
@@ -1553,7 +1583,7 @@ Layout plan(int64_t R, int64_t K, int64_t N, int32_t n_experts, moe_dtype_t x_dt
   if (L.split > 0 && tiles * L.split < 96 && kb > 24 * L.split && R <= 128 * static_cast<int64_t>(n_experts))
     L.split = 0;
   if (L.split == 0 && R > 128 * static_cast<int64_t>(n_experts))
-    L.tile_rows = R >= 512 * static_cast<int64_t>(n_experts) ? 2 * PAIR_ROWS : PAIR_ROWS;
+    L.tile_rows = tall_tiles(R, n_experts, nt) ? 2 * PAIR_ROWS : PAIR_ROWS;
   L.status = take(256);
   L.sched = take(sizeof(Sched));
   L.counters = take(sizeof(int32_t) * kMaxCtas);
