@@ -434,8 +434,9 @@ MOE_EXPORT moe_status_t moe_int8_product(const moe_int8_args_t* args, void* work
 /* out[t] = residual[t] + sum over the k slots of weights[t, s] * y[slot_pos[t, s]],
  * summed in fp32 in slot order and rounded once. y [R, d] and out [T, d] are MOE_F32
  * or MOE_BF16 (residual has out's type); weights [T, k] fp32 or NULL for 1; a slot_pos
- * outside [0, R) adds nothing. Limits: 0 <= T <= 2^24, 1 <= k <= 32, d a multiple of 8,
- * 0 <= R <= 2^29. Generalises moe_combine (k = 2, fp32 rows). */
+ * outside [0, R) adds nothing; out may be residual. Limits: 0 <= T <= 2^24, 1 <= k <= 32,
+ * d a multiple of 8 up to 2^20, T * ceil(d / 1024) < 2^31, 0 <= R <= 2^29. Generalises
+ * moe_combine (k = 2, fp32 rows). */
 MOE_EXPORT moe_status_t moe_combine_topk(const void* y, moe_dtype_t y_dtype, int64_t R, const int32_t* slot_pos,
                                          const float* weights, int64_t T, int32_t k, int64_t d,
                                          const void* residual, void* out, moe_dtype_t out_dtype,
