@@ -47,7 +47,7 @@ def moe_int8_product(x, w, s, *, x_scale=None, index=None, counts=None, w_up=Non
     x_code = N.MOE_INT8 if xt is i8 else _code(xt, "x")
     if x.shape[1] != K:
         _refuse(f"x has rows of {x.shape[1]}, w of {K}")
-    R = rows if index is None else index.shape[0]
+    R = rows if index is None else index.numel()
     if (w_up is None) != (s_up is None):
         _refuse("w_up and s_up come together")
     xp = x.data_ptr()

@@ -29,11 +29,11 @@ def _setup():
     import torch
 
     _F32, _BF16, _I32, _I8, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.int8, torch.uint8
-    _CODES.update({_F32: N.MOE_F32, _BF16: N.MOE_BF16})
     _current_device = torch.cuda.current_device
     # the handle of a device's current stream without building a stream object for it
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _CODES.update({_F32: N.MOE_F32, _BF16: N.MOE_BF16})  # last: it says that the rest is there
 
 
 def _refuse(what):

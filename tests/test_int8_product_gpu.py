@@ -246,6 +246,13 @@ def test_binding_refuses():
                              workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
 
 
+def test_binding_refuses_other_shapes_of_index():
+    c = make(40, 64, 48, 1, 3)
+    for index in (torch.tensor(3, dtype=torch.int32, device=DEV), torch.zeros((2, 20), dtype=torch.int32, device=DEV)):
+        with pytest.raises(ValueError):
+            moe.moe_int8_product(c["x"], c["w"], c["s"], index=index)
+
+
 def test_streams_and_graph():
     cs = [make(40, 512, 272, 2, 21, rows=[20, 20]), make(700, 640, 272, 2, 22, rows=[300, 400], pair=True)]
     want = [call(c) for c in cs]
