@@ -127,6 +127,27 @@ def test_activations(act, out):
     check(c, call(c, out_dtype=out, activation=ACT[act]), act)
 
 
+@pytest.mark.parametrize("act", ["gelu", "erf", "silu"])
+@pytest.mark.parametrize("R,n", [(40, 2), (700, 2)])
+def test_gate_values_whose_square_leaves_the_fp32_range(R, n, act):
+    c = make(R, 256, 272, n, 31, x="f32", pair=True, rows=[R // 2, R - R // 2])
+    c["x"] *= 1e25
+    c["s_up"] = (c["s_up"].float() * 1e-30).to(torch.bfloat16)
+    got = call(c, out_dtype=torch.float32, activation=ACT[act]).double()
+    q, a = quantised(c)
+    for e, r in enumerate((slice(0, R // 2), slice(R // 2, R))):
+        z = (q[r] @ c["w"][e].double()) * a[r, None] * c["s"][e].double()
+        z1 = (q[r] @ c["w_up"][e].double()) * a[r, None] * c["s_up"][e].double()
+        assert float(z.abs().max()) > 2.0 ** 64
+        # far from 0 every activation is z or 0 to the last bit; left are the roundings of an integer to fp32
+        # and of two scales, twice, of the activation's own steps (reciprocal 2 u, product u) and of the product
+        want = torch.where(z > 0, z, 0.0) * z1
+        sure = z.abs() > 1e3
+        assert int(sure.sum()) > 0.9 * sure.numel()
+        err = (got[r] - want).abs()
+        assert bool((err[sure] <= 12 * U * want.abs()[sure]).all()) and not bool(torch.isnan(got[r]).any())
+
+
 @pytest.mark.parametrize("R,rows", [(40, [5, 0, 7, 20]), (600, [200, 0, 100, 150])])
 def test_rows_behind_the_last_expert_stay(R, rows):
     c = make(R, 272, 144, 4, R, rows=rows, tokens=33)
