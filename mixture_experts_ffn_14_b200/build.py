@@ -9,16 +9,21 @@ source or header is newer than the object. Cross-compiles without a GPU.
 computes and another uses is checked before the access, a failed check sets
 status bit 0x40 and skips the access. Load it with
 ``MOE_B200_LIBRARY=libmoe_b200_debug.so``.
+
+``build_torch_calls`` compiles ``_torch_calls.so`` (csrc/torch_calls.cpp), the binding of
+the routing, combine and int8 calls, against the installed torch's headers.
 """
 
 from __future__ import annotations
 
 import argparse
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,6 +32,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_b200.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libmoe_b200_debug.so")
+TORCH_CALLS = os.path.join(PKG, "_torch_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + [
@@ -76,6 +82,30 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
     return lib
 
 
+def build_torch_calls(force: bool = False, verbose: bool = False) -> str:
+    src = os.path.join(CSRC, "torch_calls.cpp")
+    if not force and not _stale(TORCH_CALLS, [src] + _headers()):
+        return TORCH_CALLS
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found: its headers are required to build _torch_calls.so")
+    import torch
+
+    home = os.path.dirname(spec.origin)
+    include = os.path.join(home, "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    cmd += ["-I" + d for d in (os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], include,
+                               os.path.join(include, "torch", "csrc", "api", "include"), cuda)]
+    cmd += [src, "-o", TORCH_CALLS, "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-lc10_cuda", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    return TORCH_CALLS
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__)
     ap.add_argument("--force", action="store_true")
@@ -85,6 +115,7 @@ def main(argv=None):
                     help="build libmoe_b200_debug.so with the device-side index checks")
     a = ap.parse_args(argv)
     print(build(force=a.force, verbose=a.verbose, ptxas_info=a.ptxas_info, debug_bounds=a.debug_bounds))
+    print(build_torch_calls(force=a.force, verbose=a.verbose))
 
 
 if __name__ == "__main__":

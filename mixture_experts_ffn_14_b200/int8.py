@@ -17,7 +17,6 @@ from __future__ import annotations
 
 from . import _native as N
 from . import routed as _r
-from .routed import _check, _code, _first, _need, _on, _refuse
 
 __all__ = ["moe_int8_product", "moe_int8_workspace_size"]
 
@@ -39,46 +38,6 @@ def moe_int8_product(x, w, s, *, x_scale=None, index=None, counts=None, w_up=Non
     as they were (an output that is not given starts as zeros then). ``out_dtype``: bf16
     (the default) or fp32. ``workspace``: uint8 tensor of moe_int8_workspace_size bytes;
     moe_device_status reads its status word."""
-    dev = _first(x, "x", 2)
-    _first(w, "w", 3)
-    f32, i32, i8, b16 = _r._F32, _r._I32, _r._I8, _r._BF16
-    rows, xt = x.shape[0], x.dtype
-    n, K, cols = shape = w.shape
-    x_code = N.MOE_INT8 if xt is i8 else _code(xt, "x")
-    if x.shape[1] != K:
-        _refuse(f"x has rows of {x.shape[1]}, w of {K}")
-    R = rows if index is None else index.numel()
-    if (w_up is None) != (s_up is None):
-        _refuse("w_up and s_up come together")
-    xp = x.data_ptr()
-    ptrs = (_need(x_scale, "x_scale", (R,), f32, dev), _need(index, "index", (R,), i32, dev),
-            _need(counts, "counts", (n,), i32, dev), _need(w, "w", shape, i8, dev),
-            _need(w_up, "w_up", shape, i8, dev), _need(s, "s", (n, cols), b16, dev),
-            _need(s_up, "s_up", (n, cols), b16, dev), _need(gate, "gate", (R,), f32, dev))
-
-    def call(handle):
-        o = out
-        if o is None:
-            import torch
-
-            o = (torch.empty if counts is None else torch.zeros)((R, cols), dtype=out_dtype or b16, device=dev)
-        elif out_dtype is not None and o.dtype is not out_dtype:
-            _refuse(f"out has type {o.dtype}, not {out_dtype}")
-        dtype = o.dtype
-        out_code = _code(dtype, "out")
-        a = N.MoeInt8Args(xp, *ptrs, _need(o, "out", (R, cols), dtype, dev), rows, R, K, cols, n, x_code, out_code,
-                          activation)
-        L = N.lib()
-        if workspace is None:
-            from torch import empty
-
-            size = L.moe_int8_workspace_size(R, K, cols, n, x_code, 0 if w_up is None else 1)
-            held = empty(size, dtype=_r._U8, device=dev)
-            ws = held.data_ptr()
-        else:
-            size = workspace.numel()
-            ws = _need(workspace, "workspace", (size,), _r._U8, dev)
-        _check(L.moe_int8_product(a, ws, size, handle), "moe_int8_product")
-        return o
-
-    return _on(dev, stream, call)
+    call = (_r._calls or _r._load()).int8_product
+    args = (x, w, s, x_scale, index, counts, w_up, s_up, activation, gate, out, out_dtype, workspace)
+    return call(*args) if stream is None else _r._on(stream, x, call, args)
