@@ -2,9 +2,10 @@
 // (moe_topk_route), its backward pass and the dispatch of its choice.
 //
 // One warp takes one token. Lane L holds the logits of the experts L * VPL ..
-// L * VPL + VPL - 1 (VPL = E / 32 rounded up to a power of two), so that a group of
-// experts is a run of lanes and "the lower expert" is the lower lane, then the
-// lower register.
+// L * VPL + VPL - 1 (VPL = E / 32 rounded up to a power of two). With groups each group
+// has a run of lanes of its own (32 lanes over the groups, rounded to powers of two), so
+// that what is asked of a group is a reduction within its run. "The lower expert" is the
+// lower lane, then the lower register.
 //
 // Bound by instructions, not by the logits' bytes (16384 tokens x 256 experts: 16.8 MB,
 // 2.6 us at the copy rate), so the common path is built of few of them. A rank value
@@ -43,7 +44,8 @@ struct TopkParams {
   const int32_t* n_tokens;
   int64_t T;
   int32_t E, k, n_groups, topk_groups, group_size, score, rule, renorm;
-  int32_t lane_run;     // lanes per group if that is a whole power of two, else 0
+  int32_t lane_run;     // lanes per group (a power of two); 0: one group, or too many for runs
+  int32_t run_shift;    // its logarithm
   float scale;
   int32_t* idx;
   float* weights;
@@ -77,14 +79,27 @@ __device__ __forceinline__ float load_logit(const void* logits, int64_t at) {
   return clean(static_cast<const float*>(logits)[at]);
 }
 
-// Logits of this lane's experts; -inf past the last one. Rows whose start and
-// length are whole vectors load 16 bytes at a time.
+// Experts of a lane: `first`, and the end of those it may hold (those of its group, or all).
+struct LaneExperts {
+  int first, end;
+};
+template <int VPL>
+__device__ __forceinline__ LaneExperts lane_experts(const TopkParams& p, int lane) {
+  if (p.lane_run == 0) return {lane * VPL, p.E};
+  const int g = lane >> p.run_shift;
+  if (g >= p.n_groups) return {p.E, p.E};
+  return {g * p.group_size + (lane & (p.lane_run - 1)) * VPL, (g + 1) * p.group_size};
+}
+
+// Logits of this lane's experts; -inf past the last one. Where rows and groups (of `unit`
+// experts) are whole vectors, 16 bytes at a time.
 template <bool BF16, int VPL>
-__device__ __forceinline__ void load_row(const void* logits, int64_t t, int E, int lane, float (&l)[VPL]) {
-  const int64_t row = t * E;
-  const int e0 = lane * VPL;
+__device__ __forceinline__ void load_row(const void* logits, int64_t t, int row_len, int unit, LaneExperts mine,
+                                         float (&l)[VPL]) {
+  const int64_t row = t * row_len;
+  const int e0 = mine.first, E = mine.end;
   constexpr int PER = BF16 ? 8 : 4;
-  if (VPL >= PER && E % PER == 0) {
+  if (VPL >= PER && unit % PER == 0) {
 #pragma unroll
     for (int v = 0; v < (VPL >= PER ? VPL / PER : 0); ++v) {
       const int e = e0 + v * PER;
@@ -114,11 +129,11 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t t, int E, i
   }
 }
 
-// Biases of this lane's experts (0 past the last one).
+// Biases of this lane's experts (left as they are past the last one).
 template <int VPL>
-__device__ __forceinline__ void load_bias(const float* bias, int E, int lane, float (&b)[VPL]) {
-  const int e0 = lane * VPL;
-  if (VPL >= 4 && E % 4 == 0) {
+__device__ __forceinline__ void load_bias(const float* bias, int unit, LaneExperts mine, float (&b)[VPL]) {
+  const int e0 = mine.first, E = mine.end;
+  if (VPL >= 4 && unit % 4 == 0) {
 #pragma unroll
     for (int v = 0; v < VPL / 4; ++v)
       if (e0 + 4 * v < E) {
@@ -289,7 +304,7 @@ __device__ __forceinline__ unsigned kept_groups_exact(const TopkParams& p, int l
 }
 
 template <int VPL>
-__device__ __forceinline__ int take_k_exact(uint64_t* key, int k, int lane) {
+__device__ __forceinline__ int take_k_exact(uint64_t* key, int k, int lane, int e0) {
   int pick = -1;
 #pragma unroll 1
   for (int i = 0; i < k; ++i) {
@@ -303,7 +318,7 @@ __device__ __forceinline__ int take_k_exact(uint64_t* key, int k, int lane) {
       }
     int src;
     if (warp_best64(best, src) < kFirstKey64) break;
-    const int e = __shfl_sync(kFull, lane * VPL + at, src);
+    const int e = __shfl_sync(kFull, e0 + at, src);
     if (lane == i) pick = e;
     if (lane == src) key[at] = 0;
   }
@@ -352,9 +367,9 @@ __device__ constexpr float key_slack() {
   return 1.2e-7f * VPL + 1.2e-7f;
 }
 
-// The same from 64-bit values, for groups that are runs of lanes with sorted keys: every
-// lane scores those of its experts again that may be one of the group's two largest (a, b:
-// the group's two largest keys), one after the other.
+// The same from 64-bit values, for groups that are runs of lanes: every lane scores those
+// of its experts again that may be one of the group's two largest (a, b: the group's two
+// largest keys), one after the other.
 template <bool BF16, int VPL>
 __device__ __noinline__ unsigned settle_groups(const TopkParams& p, int64_t t, int lane, const uint32_t (&key)[VPL],
                                                bool by_score, float err, uint32_t a, uint32_t b) {
@@ -366,6 +381,7 @@ __device__ __noinline__ unsigned settle_groups(const TopkParams& p, int64_t t, i
     limit = v - 2.0f * err - 3.0f * key_slack<VPL>() * fabsf(v);
   }
   const ExactRow row = by_score ? exact_row<BF16, VPL>(p, t, lane) : ExactRow{};
+  const int e0 = lane_experts<VPL>(p, lane).first;
   uint64_t c = 0, d = 0;
   for (int j = 0; j < VPL; ++j) {
     uint32_t k = kNoKey;
@@ -373,9 +389,12 @@ __device__ __noinline__ unsigned settle_groups(const TopkParams& p, int64_t t, i
     for (int i = 0; i < VPL; ++i)
       if (i == j) k = key[i];
     const bool look = k >= kFirstKey && bare_value<VPL>(k) >= limit;
-    if (!__any_sync(kFull, look)) break;
+    if (!__any_sync(kFull, look)) {
+      if (VPL <= 8) break;  // sorted keys: none further on either
+      continue;
+    }
     if (look) {
-      const double v = exact_value<BF16>(p, t, lane * VPL + VPL - 1 - static_cast<int>(k & (VPL - 1)), by_score, row);
+      const double v = exact_value<BF16>(p, t, e0 + VPL - 1 - static_cast<int>(k & (VPL - 1)), by_score, row);
       push2(c, d, order_key64(v));
     }
     __syncwarp();
@@ -402,8 +421,8 @@ __device__ __noinline__ unsigned settle_groups(const TopkParams& p, int64_t t, i
 // Bits of the leaders of the groups that stay (lane g for group g, or the first lane of
 // its run where groups are whole runs of lanes), from the keys the groups go by.
 // Where two groups on either side of the limit are closer than their errors, the groups
-// are valued again in 64 bits; `undecided` is set when that takes more than the sorted
-// keys of whole lanes.
+// are valued again in 64 bits; `undecided` is set where groups are no runs of lanes, or
+// values infinite.
 template <bool BF16, int VPL>
 __device__ __forceinline__ unsigned kept_groups(const TopkParams& p, int64_t t, int lane, const uint32_t (&key)[VPL],
                                                 bool by_score, float err, bool& undecided) {
@@ -473,7 +492,7 @@ __device__ __forceinline__ unsigned kept_groups(const TopkParams& p, int64_t t, 
     const float sizes = __shfl_sync(kFull, size, src) + __shfl_sync(kFull, size, next);
     // an empty group is exact
     if (high != -INFINITY && !(low - high > 4.0f * err + key_slack<VPL>() * sizes)) {
-      if (!kSorted || p.lane_run == 0 || !(sizes < INFINITY)) undecided = true;
+      if (p.lane_run == 0 || !(sizes < INFINITY)) undecided = true;
       else kept = settle_groups<BF16, VPL>(p, t, lane, key, by_score, err, a, b);
     }
   }
@@ -567,14 +586,14 @@ __device__ __forceinline__ void take_k(const TopkParams& p, int64_t t, uint32_t 
         near_next = close();
         m = k < 31 && !((near_next >> k) & 1u) ? k + 1 : 0;
       }
-      pick = has ? from * VPL + (VPL - 1 - static_cast<int>(mine & kIndex)) : -1;
+      pick = has ? lane_experts<VPL>(p, from).first + (VPL - 1 - static_cast<int>(mine & kIndex)) : -1;
       if (m == 0 || __any_sync(kFull, has && !(fabsf(key_value(mine)) < INFINITY))) undecided = true;
       else pick = settle_order<BF16, VPL>(p, t, lane, pick, min(m, __popc(__ballot_sync(kFull, has))), by_score);
       if (lane >= k) pick = -1;
       return;
     }
   }
-  pick = has && lane < k ? from * VPL + (VPL - 1 - static_cast<int>(mine & kIndex)) : -1;
+  pick = has && lane < k ? lane_experts<VPL>(p, from).first + (VPL - 1 - static_cast<int>(mine & kIndex)) : -1;
 }
 
 // Scores of this lane's experts, the row's largest logit and, for softmax, the sum.
@@ -649,6 +668,7 @@ template <bool BF16, int VPL>
 __device__ __noinline__ int choose_exact(const TopkParams& p, int64_t t, int lane) {
   const bool biased = p.bias != nullptr, sums = p.n_groups > 1 && p.rule == MOE_GROUP_TOP2_SUM;
   const ExactRow row = biased || sums ? exact_row<BF16, VPL>(p, t, lane) : ExactRow{};
+  const LaneExperts own = lane_experts<VPL>(p, lane);
   uint64_t key[VPL];
   unsigned kept = kFull;
 #pragma unroll 1
@@ -656,9 +676,9 @@ __device__ __noinline__ int choose_exact(const TopkParams& p, int64_t t, int lan
     const bool by_score = biased || (pass == 0 && sums);
 #pragma unroll 1
     for (int j = 0; j < VPL; ++j) {
-      const int e = lane * VPL + j;
+      const int e = own.first + j;
       uint64_t k = 0;
-      if (e < p.E && load_logit<BF16>(p.logits, t * p.E + e) > -INFINITY) {
+      if (e < own.end && load_logit<BF16>(p.logits, t * p.E + e) > -INFINITY) {
         const double v = exact_value<BF16>(p, t, e, by_score, row);
         if (!(v != v)) k = order_key64(v);
       }
@@ -675,7 +695,7 @@ __device__ __noinline__ int choose_exact(const TopkParams& p, int64_t t, int lan
       if (g >= 32 || !((kept >> g) & 1u)) key[j] = 0;
     }
   }
-  return take_k_exact<VPL>(key, p.k, lane);
+  return take_k_exact<VPL>(key, p.k, lane, own.first);
 }
 
 // Share of each choice in the renormalised weights (P lanes of a warp, a power of two,
@@ -697,7 +717,8 @@ __device__ __forceinline__ float share_of(int score, float lv, int P) {
 template <bool BF16, int VPL>
 __device__ __forceinline__ int choose(const TopkParams& p, int64_t t, int lane, float& top, float& z) {
   float l[VPL];
-  load_row<BF16, VPL>(p.logits, t, p.E, lane, l);
+  const LaneExperts own = lane_experts<VPL>(p, lane);
+  load_row<BF16, VPL>(p.logits, t, p.E, p.group_size, own, l);
   const bool groups = p.n_groups > 1, sums = groups && p.rule == MOE_GROUP_TOP2_SUM;
   const bool biased = p.bias != nullptr;
   float s[VPL], s_top = 1.0f;
@@ -705,7 +726,7 @@ __device__ __forceinline__ int choose(const TopkParams& p, int64_t t, int lane, 
     row_scores<VPL>(p.score, l, s, top, z);
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
-      if (lane * VPL + j < p.E) p.scores[t * p.E + lane * VPL + j] = s[j];
+      if (own.first + j < own.end) p.scores[t * p.E + own.first + j] = s[j];
     if (p.score == MOE_SCORE_SOFTMAX) s_top = 1.0f / z;
   } else if (biased || sums || (p.score == MOE_SCORE_SOFTMAX && p.renorm == 0)) {
     rank_scores<VPL>(p.score, l, s, s_top, top, z);
@@ -717,7 +738,7 @@ __device__ __forceinline__ int choose(const TopkParams& p, int64_t t, int lane, 
     float bias[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) bias[j] = 0.0f;
-    if (biased) load_bias<VPL>(p.bias, p.E, lane, bias);
+    if (biased) load_bias<VPL>(p.bias, p.group_size, own, bias);
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       // 0 * l: NaN for a masked expert; the maximum turns NaN into -inf
@@ -1107,8 +1128,9 @@ __global__ void __launch_bounds__(kGradWarps * 32) moe_topk_grad_kernel(const __
     for (int j = 0; j < VPL; ++j) d[j] = 0.0f;
     if (t < n) {
       float l[VPL], c[VPL];
-      load_row<BF16, VPL>(p.logits, t, p.E, lane, l);
-      if (p.grad_scores != nullptr) load_bias<VPL>(p.grad_scores + t * p.E, p.E, lane, d);
+      const LaneExperts own{lane * VPL, p.E};
+      load_row<BF16, VPL>(p.logits, t, p.E, p.E, own, l);
+      if (p.grad_scores != nullptr) load_bias<VPL>(p.grad_scores + t * p.E, p.E, own, d);
 #pragma unroll
       for (int j = 0; j < VPL; ++j) c[j] = mine[i][lane * VPL + j];
       // renormalised weights reach the logits directly, the others through the scores
@@ -1139,14 +1161,14 @@ __global__ void __launch_bounds__(kGradWarps * 32) moe_topk_grad_kernel(const __
   }
 }
 
-// Calls f with the registers per lane for E experts as a constant.
+// Calls f with the registers per lane as a constant: those that `per_lane` experts take.
 template <typename F>
-cudaError_t with_vpl(int E, F f) {
-  if (E <= 32) return f(std::integral_constant<int, 1>{});
-  if (E <= 64) return f(std::integral_constant<int, 2>{});
-  if (E <= 128) return f(std::integral_constant<int, 4>{});
-  if (E <= 256) return f(std::integral_constant<int, 8>{});
-  if (E <= 512) return f(std::integral_constant<int, 16>{});
+cudaError_t with_vpl(int per_lane, F f) {
+  if (per_lane <= 1) return f(std::integral_constant<int, 1>{});
+  if (per_lane <= 2) return f(std::integral_constant<int, 2>{});
+  if (per_lane <= 4) return f(std::integral_constant<int, 4>{});
+  if (per_lane <= 8) return f(std::integral_constant<int, 8>{});
+  if (per_lane <= 16) return f(std::integral_constant<int, 16>{});
   return f(std::integral_constant<int, 32>{});
 }
 
@@ -1256,11 +1278,25 @@ moe_status_t moe_topk_route(const moe_topk_args_t* a, const moe_topk_routed_t* r
   const unsigned grid = static_cast<unsigned>(L.nblk);
   const bool few = L.nblk <= device_sm_count();
   const bool cluster = dispatch && L.nblk > 1 && L.nblk <= kClusterBlocks;
-  const cudaError_t e = with_vpl(a->E, [&](auto v) {
+  // Lanes of a group: 32 over the number of groups, rounded to a power of two. A group count
+  // that is none can need more registers than the largest kernel has; then groups lie
+  // across lanes.
+  int per_lane = (a->E + 31) / 32;
+  if (a->n_groups > 1) {
+    int run = 32, shift = 5;
+    while (run > 1 && run * a->n_groups > 32) {
+      run /= 2;
+      --shift;
+    }
+    if ((p.group_size + run - 1) / run <= 32) {
+      per_lane = (p.group_size + run - 1) / run;
+      p.lane_run = run;
+      p.run_shift = shift;
+    }
+  }
+  const cudaError_t e = with_vpl(per_lane, [&](auto v) {
     constexpr int VPL = decltype(v)::value;
     constexpr int WIDE = VPL <= 8 ? 32 : 16;
-    const int run = p.group_size / VPL;
-    p.lane_run = p.group_size % VPL == 0 && (run & (run - 1)) == 0 ? run : 0;
     const unsigned threads = few ? WIDE * 32 : 8 * 32, blocks = cluster ? grid : 1;
     if (a->dtype == MOE_BF16)
       return few ? launch_kernel(moe_topk_route_kernel<true, VPL, WIDE>, grid, threads, 0, s, blocks, false, p)
@@ -1288,7 +1324,7 @@ moe_status_t moe_topk_route_backward(const moe_topk_args_t* a, const int32_t* id
   TopkGradParams p{a->logits, a->n_tokens, idx, grad_weights, grad_scores, grad_logits, a->T, a->E,
                    a->k,      a->score,    a->renormalize, a->scale,     1};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = with_vpl(a->E, [&](auto v) {
+  const cudaError_t e = with_vpl((a->E + 31) / 32, [&](auto v) {
     constexpr int VPL = decltype(v)::value;
     // one token per warp while that leaves SMs with less than two CTAs (4096 tokens of 8
     // experts: 4.6 us with one, 6.3 with four; 16384 of 256: 14.1 and 13.3)

@@ -405,3 +405,75 @@ def test_route_single_near_ties(kind, E, k, groups, keep):
                 e = torch.tensor(order[at:at + width], device=DEV)
                 l[e] += torch.arange(width, device=DEV) * 2.0 ** -21
             run_and_check(l[None].contiguous(), k, kind, groups=groups, keep=keep, rule="max")
+
+
+def test_binding_refuses_what_the_c_types_would_cut():
+    logits = torch.zeros((4, 8), device=DEV)
+    for bad in (dict(k=2 ** 32 + 2), dict(k=2, n_groups=2 ** 40), dict(k=2, out=[]), dict(k=2, bias=[0.0] * 8),
+                dict(k=2, out={"idx": torch.zeros((4, 2), dtype=torch.int32, device=DEV), "other": None})):
+        with pytest.raises(ValueError):
+            moe.moe_topk_route(logits, **bad)
+    with pytest.raises(TypeError):
+        moe.moe_topk_route(logits, 2.5)
+    with pytest.raises(ValueError):
+        moe.moe_topk_route(logits, 2, workspace=torch.zeros(256, device=DEV))
+    with pytest.raises(moe.MoeError):
+        moe.moe_topk_route(logits, 9)
+    kept = torch.full((4, 2), 5, dtype=torch.int32, device=DEV)
+    r = moe.moe_topk_route(logits, 2, out={"idx": kept, "weights": None}, dispatch=False)
+    assert r["idx"] is kept and list(r) == ["idx", "weights"]
+    assert kept.tolist() == [[0, 1]] * 4
+
+
+def test_binding_allocates_on_the_stream_it_is_given():
+    y, pos = torch.ones((64, 64), device=DEV), torch.arange(64, dtype=torch.int32, device=DEV).view(32, 2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        out = moe.moe_combine_topk(y, pos, stream=stream)
+        side.synchronize()
+        assert bool((out == 2).all()) and torch.cuda.current_stream() != side
+
+
+# Group sizes that are no powers of two, groups with idle lanes, more than 8 registers per
+# lane, and the two that do not fit runs of lanes (9 x 113, 24 x 40).
+ODD_GROUPS = [(136, 8, 3), (88, 8, 6), (44, 4, 2), (100, 5, 2), (6, 2, 1), (250, 2, 1), (348, 4, 3), (504, 8, 6),
+              (512, 8, 6), (960, 24, 7), (1017, 9, 4), (31, 31, 5), (693, 11, 5)]
+
+
+@pytest.mark.parametrize("E,groups,keep", ODD_GROUPS)
+@pytest.mark.parametrize("rule", ["max", "top2"])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_route_groups_of_odd_sizes(E, groups, keep, rule, kind, dtype):
+    k = min(9, E // groups * keep)
+    for masked, T in ((0.2, 200), (0.9, 33)):
+        l = logits_of(T, E, dtype, E + groups, masked=masked)
+        for bias in (None, torch.randn(E, generator=gen(E), device=DEV) * 0.1):
+            run_and_check(l, k, kind, bias=bias, groups=groups, keep=keep, rule=rule, renorm=dtype == torch.bfloat16,
+                          want_scores=T == 33)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,keep", [(136, 8, 3), (512, 8, 6), (504, 8, 3), (1024, 4, 2), (100, 5, 2), (960, 24, 7)])
+def test_route_near_ties_in_groups_of_odd_sizes(kind, E, groups, keep):
+    """score + bias equal up to the rounding of the bias, in every expert, in a few, and in the two
+    largest of each group."""
+    k, gs = 6, E // groups
+    g = gen(E)
+    row = torch.randn(E, generator=g, device=DEV)
+    _, _, s = ref.scores(row.double().cpu().numpy()[None], kind)
+    order = torch.randperm(E, generator=g, device=DEV).cpu().numpy()
+    flat = np.ones(E)
+    few = 3.0 - 0.01 * order
+    few[order[:5]] = few[order[0]]
+    heads = 1.0 - 0.01 * (np.arange(E) % gs)
+    heads[np.arange(E) % gs == min(1, gs - 1)] = 1.0
+    for c in (flat, few, heads):
+        bias = torch.from_numpy((c - s[0]).astype(np.float32)).to(DEV)
+        for rule in ("max", "top2"):
+            run_and_check(row.repeat(3, 1), k, kind, bias=bias, groups=groups, keep=keep, rule=rule)
+    l = torch.from_numpy(few.astype(np.float32)).to(DEV).repeat(2, 1)
+    l[1] += torch.arange(E, device=DEV) * 2.0 ** -21
+    for rule in ("max", "top2"):
+        run_and_check(l, k, kind, groups=groups, keep=keep, rule=rule)
