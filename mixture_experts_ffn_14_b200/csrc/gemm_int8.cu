@@ -37,6 +37,7 @@ using tc::warp_wait;
 constexpr int BK = 128;              // K per stage: 128 bytes = one swizzle row
 constexpr int WBOX = BK * 128;       // 16 KB: [128 K x 128 columns]
 constexpr int kMaxExperts = 1024;
+constexpr int64_t kEarlyBytes = 32 << 20;  // stream form: weights up to which it starts during the preparation
 constexpr int kMaxCtas = 160;        // product CTAs at most (workspace sizing; 148 SMs on B200)
 // Split form: CTAs per tile, and the clusters of that many that run at once with a margin
 // of one (one CTA per SM: 15, 22, 26, 33, 45 and 74 fit on the eight GPCs of a B200). One
@@ -503,6 +504,7 @@ struct StreamCfg {
 };
 constexpr int XBOX_ROWS = 32;
 constexpr int kMinRun = 4;  // K blocks of a run at least: 512 of K
+constexpr int kJoin = 8, kJoinHidden = 3;  // what joining the parts of a tile costs, in K blocks
 
 struct Seg {
   int e, row0, rows, n0, kb0, kb1;
@@ -548,6 +550,7 @@ __global__ void __launch_bounds__(256, 1)
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
+  wait_prerequisites();  // the schedule and the quantised rows
   for (int e = threadIdx.x; e <= p.n_experts; e += 256) {
     pre[e] = p.sched->pre[e];
     off[e] = p.sched->off[e];
@@ -563,8 +566,11 @@ __global__ void __launch_bounds__(256, 1)
   const int64_t tiles = static_cast<int64_t>(pre[p.n_experts]) * p.nt;
   const int64_t waves = tiles / gridDim.x, whole0 = tiles - waves * gridDim.x;
   const int64_t total = whole0 * p.kb;  // K blocks of the cut part
-  // Runs of at least kMinRun K blocks: no run is empty, the last CTAs may have none.
-  const int64_t G = min(static_cast<int64_t>(gridDim.x), max(total / kMinRun, int64_t(1)));
+  // Runs of at least kMinRun K blocks: no run is empty, the last CTAs may have none. Whole
+  // tiles, one to a CTA, where cutting would shorten the longest run by less than joining
+  // costs: kJoin K blocks, or kJoinHidden behind whole tiles.
+  int64_t G = min(static_cast<int64_t>(gridDim.x), max(total / kMinRun, int64_t(1)));
+  if (p.kb - (total + G - 1) / G <= (waves == 0 ? kJoin : kJoinHidden)) G = whole0;
   const int64_t me = blockIdx.x;
   const int64_t lo = me < G ? total * me / G : total, hi = me < G ? total * (me + 1) / G : total;
 
@@ -710,7 +716,7 @@ __global__ void __launch_bounds__(256, 1)
         const int64_t row = s.row0 + 32 * i + lane;
         const bool in = 32 * i + lane < s.rows;
         // the row's scale, and with the gate: of the up product, or of the only one
-        ra[i] = in ? __ldg(p.a + row) : 0.0f;
+        ra[i] = in ? p.a[row] : 0.0f;  // may be written while this kernel starts: not a read-only load
         rg[i] = in && p.gate != nullptr ? ra[i] * __ldg(p.gate + row) : ra[i];
         if (!DUAL) ra[i] = rg[i];
       }
@@ -1653,7 +1659,10 @@ cudaError_t launch_stream(const moe_int8_args_t* a, const void* q, Params p, int
   }
   const int64_t most = ((a->R + ROWS - 1) / ROWS + a->n_experts) * p.nt * p.kb;
   const int grid = static_cast<int>(std::min<int64_t>(std::min(device_sm_count(), kMaxCtas), most));
-  return launch_kernel(kern, grid, 256, kSmem, s, 1, false, tx, tw0, tw1, p);
+  // Started while the rows are prepared where weights take microseconds; with more of them
+  // CTAs that start apart lose the DRAM pages that neighbours share (5 to 8 %).
+  const int64_t weights = a->n_experts * a->K * a->N * (DUAL ? 2 : 1);
+  return launch_kernel(kern, grid, 256, kSmem, s, 1, dependent && weights <= kEarlyBytes, tx, tw0, tw1, p);
 }
 
 template <int H, bool DUAL, bool OB>

@@ -27,6 +27,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "moe_internal.cuh"
 #include "sm100.cuh"
@@ -91,63 +92,65 @@ __device__ __forceinline__ LaneExperts lane_experts(const TopkParams& p, int lan
   return {g * p.group_size + (lane & (p.lane_run - 1)) * VPL, (g + 1) * p.group_size};
 }
 
-// Logits of this lane's experts; -inf past the last one. Where rows and groups (of `unit`
-// experts) are whole vectors, 16 bytes at a time.
+// W values of a type next to one another in memory, as one access.
+template <typename T, int W>
+struct alignas(sizeof(T) * W) Pack {
+  T v[W];
+};
+
+// Calls f with the widest access (16 bytes at most) that divides a lane's registers and
+// `unit` experts: all rows and lanes then start on its boundary. (Rows of 372 bf16 logits
+// one by one: gradient of 11275 tokens 36 us a call.)
+template <int VPL, int MOST, typename F>
+__device__ __forceinline__ void with_width(int unit, F f) {
+  if constexpr (MOST > VPL) {
+    with_width<VPL, MOST / 2>(unit, f);
+  } else if constexpr (MOST == 1) {
+    f(std::integral_constant<int, 1>{});
+  } else {
+    if (unit % MOST == 0) f(std::integral_constant<int, MOST>{});
+    else with_width<VPL, MOST / 2>(unit, f);
+  }
+}
+
+// Logits of this lane's experts; -inf past the last one.
 template <bool BF16, int VPL>
 __device__ __forceinline__ void load_row(const void* logits, int64_t t, int row_len, int unit, LaneExperts mine,
                                          float (&l)[VPL]) {
-  const int64_t row = t * row_len;
-  const int e0 = mine.first, E = mine.end;
-  constexpr int PER = BF16 ? 8 : 4;
-  if (VPL >= PER && unit % PER == 0) {
+  using T = std::conditional_t<BF16, uint16_t, float>;
+  const T* at = static_cast<const T*>(logits) + t * row_len + mine.first;
+  with_width<VPL, 16 / sizeof(T)>(unit, [&](auto width) {
+    constexpr int W = decltype(width)::value;
 #pragma unroll
-    for (int v = 0; v < (VPL >= PER ? VPL / PER : 0); ++v) {
-      const int e = e0 + v * PER;
-      if (e < E) {
-        if (BF16) {
-          const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(logits) + row + e);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int v = 0; v < VPL; v += W) {
+      if (mine.first + v < mine.end) {
+        const Pack<T, W> w = *reinterpret_cast<const Pack<T, W>*>(at + v);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            l[(v * PER + 2 * j) % VPL] = clean(__uint_as_float(w[j] << 16));
-            l[(v * PER + 2 * j + 1) % VPL] = clean(__uint_as_float(w[j] & 0xFFFF0000u));
-          }
-        } else {
-          const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(logits) + row + e);
-          const float w[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) l[(v * PER + j) % VPL] = clean(w[j]);
+        for (int j = 0; j < W; ++j) {
+          if constexpr (BF16) l[v + j] = clean(__uint_as_float(static_cast<uint32_t>(w.v[j]) << 16));
+          else l[v + j] = clean(w.v[j]);
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) l[(v * PER + j) % VPL] = -INFINITY;
+        for (int j = 0; j < W; ++j) l[v + j] = -INFINITY;
       }
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) l[j] = e0 + j < E ? load_logit<BF16>(logits, row + e0 + j) : -INFINITY;
-  }
+  });
 }
 
 // Biases of this lane's experts (left as they are past the last one).
 template <int VPL>
 __device__ __forceinline__ void load_bias(const float* bias, int unit, LaneExperts mine, float (&b)[VPL]) {
-  const int e0 = mine.first, E = mine.end;
-  if (VPL >= 4 && unit % 4 == 0) {
+  with_width<VPL, 4>(unit, [&](auto width) {
+    constexpr int W = decltype(width)::value;
 #pragma unroll
-    for (int v = 0; v < VPL / 4; ++v)
-      if (e0 + 4 * v < E) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(bias + e0) + v);
-        b[(4 * v) % VPL] = f.x;
-        b[(4 * v + 1) % VPL] = f.y;
-        b[(4 * v + 2) % VPL] = f.z;
-        b[(4 * v + 3) % VPL] = f.w;
-      }
-  } else {
+    for (int v = 0; v < VPL; v += W) {
+      if (mine.first + v >= mine.end) continue;
+      const Pack<float, W> w = *reinterpret_cast<const Pack<float, W>*>(bias + mine.first + v);
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (e0 + j < E) b[j] = __ldg(bias + e0 + j);
-  }
+      for (int j = 0; j < W; ++j) b[v + j] = w.v[j];
+    }
+  });
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -383,16 +386,16 @@ __device__ __noinline__ unsigned settle_groups(const TopkParams& p, int64_t t, i
   const ExactRow row = by_score ? exact_row<BF16, VPL>(p, t, lane) : ExactRow{};
   const int e0 = lane_experts<VPL>(p, lane).first;
   uint64_t c = 0, d = 0;
+  uint32_t below = 0xffffffffu;
   for (int j = 0; j < VPL; ++j) {
+    // the lane's largest key below the last one (keys of a lane differ in their index bits)
     uint32_t k = kNoKey;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (i == j) k = key[i];
+      if (key[i] < below) k = max(k, key[i]);
+    below = k;
     const bool look = k >= kFirstKey && bare_value<VPL>(k) >= limit;
-    if (!__any_sync(kFull, look)) {
-      if (VPL <= 8) break;  // sorted keys: none further on either
-      continue;
-    }
+    if (!__any_sync(kFull, look)) break;
     if (look) {
       const double v = exact_value<BF16>(p, t, e0 + VPL - 1 - static_cast<int>(k & (VPL - 1)), by_score, row);
       push2(c, d, order_key64(v));
@@ -1036,38 +1039,26 @@ constexpr int kGradWarps = 8;
 // after the other in slot order.
 __host__ __device__ constexpr int grad_tokens(int vpl) { return vpl <= 8 ? 4 : (vpl == 16 ? 2 : 1); }
 
-// Values of this lane's experts to memory, 16 bytes at a time where rows allow it.
+// Values of this lane's experts to memory.
 template <bool BF16, int VPL>
 __device__ __forceinline__ void store_row(void* out, int64_t t, int E, int lane, const float (&d)[VPL]) {
-  const int64_t row = t * E;
+  using T = std::conditional_t<BF16, uint16_t, float>;
   const int e0 = lane * VPL;
-  constexpr int PER = BF16 ? 8 : 4;
-  if (VPL >= PER && E % PER == 0) {
+  T* at = static_cast<T*>(out) + t * E + e0;
+  with_width<VPL, 16 / sizeof(T)>(E, [&](auto width) {
+    constexpr int W = decltype(width)::value;
 #pragma unroll
-    for (int v = 0; v < (VPL >= PER ? VPL / PER : 0); ++v) {
-      if (e0 + v * PER >= E) continue;
-      if (BF16) {
-        uint32_t w[4];
+    for (int v = 0; v < VPL; v += W) {
+      if (e0 + v >= E) continue;
+      Pack<T, W> w;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(d[(v * PER + 2 * j) % VPL], d[(v * PER + 2 * j + 1) % VPL]);
-          w[j] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + row + e0 + v * PER) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-        *reinterpret_cast<float4*>(static_cast<float*>(out) + row + e0 + v * PER) =
-            make_float4(d[(v * PER) % VPL], d[(v * PER + 1) % VPL], d[(v * PER + 2) % VPL], d[(v * PER + 3) % VPL]);
+      for (int j = 0; j < W; ++j) {
+        if constexpr (BF16) w.v[j] = __bfloat16_as_ushort(__float2bfloat16_rn(d[v + j]));
+        else w.v[j] = d[v + j];
       }
+      *reinterpret_cast<Pack<T, W>*>(at + v) = w;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      if (e0 + j >= E) continue;
-      if (BF16) static_cast<__nv_bfloat16*>(out)[row + e0 + j] = __float2bfloat16_rn(d[j]);
-      else static_cast<float*>(out)[row + e0 + j] = d[j];
-    }
-  }
+  });
 }
 
 template <bool BF16, int VPL>
