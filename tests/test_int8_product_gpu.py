@@ -119,6 +119,17 @@ def test_sizes(R, K, N, rows, x, out, pair):
     check(c, call(c, out_dtype=out))
 
 
+@pytest.mark.parametrize("K", [2176, 6144])     # whole tiles, and tiles cut into runs of K blocks
+@pytest.mark.parametrize("R,N,rows", [(20, 8192, [5, 0, 15]), (20, 19216, [5, 0, 15]), (290, 4624, [100, 128, 2, 60])])
+@pytest.mark.parametrize("pair", [False, True])
+def test_tiles_of_several_ctas(R, N, rows, K, pair):
+    c = make(R, K, N, len(rows), R + N, pair=pair, rows=rows, tokens=11)
+    ws = torch.empty(moe.moe_int8_workspace_size(R, K, N, len(rows), moe.MOE_BF16, pair), dtype=torch.uint8, device=DEV)
+    outs = [call(c, workspace=ws) for _ in range(3)]      # one workspace, one call after the other
+    check(c, outs[0])
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
 @pytest.mark.parametrize("act", ["gelu", "erf", "silu"])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["obf16", "of32"])
 def test_activations(act, out):
