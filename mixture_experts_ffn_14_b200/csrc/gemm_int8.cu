@@ -405,19 +405,22 @@ __global__ void __launch_bounds__(kPrepCta) moe_int8_prepare_long_kernel(const _
   }
   const int64_t r = static_cast<int64_t>(blockIdx.x) - 1;
   const int64_t src = p.index != nullptr ? p.index[r] : r;
-  const bool real = src >= 0 && src < p.x_rows;
   const int nvec = static_cast<int>(p.K / 8);
-  const void* row = static_cast<const uint8_t*>(p.x) + (real ? src : 0) * p.K * (BF16 ? 2 : 4);
+  uint2* dst = reinterpret_cast<uint2*>(p.q + r * p.K);
+  if (src < 0 || src >= p.x_rows) {  // a row of zeros: x may hold no row at all
+    for (int v = threadIdx.x; v < nvec; v += kPrepCta) dst[v] = make_uint2(0, 0);
+    if (threadIdx.x == 0) p.a[r] = 0.0f;
+    return;
+  }
+  const void* row = static_cast<const uint8_t*>(p.x) + src * p.K * (BF16 ? 2 : 4);
   uint32_t top_bits = 0;
-  if (real)
-    for (int v = threadIdx.x; v < nvec; v += kPrepCta) largest<BF16>(load_raw<BF16>(row, v), top_bits);
+  for (int v = threadIdx.x; v < nvec; v += kPrepCta) largest<BF16>(load_raw<BF16>(row, v), top_bits);
   top_bits = __reduce_max_sync(0xffffffffu, largest_bits<BF16>(top_bits));
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top_bits;
   __syncthreads();
   top_bits = __reduce_max_sync(0xffffffffu, part[threadIdx.x % (kPrepCta / 32)]);
   const RowScale rs(top_bits);
   if (threadIdx.x == 0) p.a[r] = row_step(top_bits);
-  uint2* dst = reinterpret_cast<uint2*>(p.q + r * p.K);
   for (int v = threadIdx.x; v < nvec; v += kPrepCta)
     dst[v] = quantise8<BF16>(load_raw<BF16>(row, v), rs);
 }

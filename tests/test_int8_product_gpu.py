@@ -228,6 +228,23 @@ def test_largest_sums():
     assert torch.equal(got, want.expand(5, 32))
 
 
+@pytest.mark.parametrize("x", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("K", [64, 2048, 33024])   # rows that pass through shared memory, and rows read twice
+def test_rows_of_an_index_that_names_none(x, K):
+    # x without a single row: there is no address that may be read
+    R, N = 6, 48
+    w = torch.randint(-128, 128, (1, K, N), device=DEV, dtype=torch.int8)
+    s = torch.ones((1, N), device=DEV, dtype=torch.bfloat16)
+    index = torch.tensor([-1, 0, 7, -(2 ** 31), 2 ** 31 - 1, 1], dtype=torch.int32, device=DEV)
+    out = torch.full((R, N), 3.0, device=DEV)
+    moe.moe_int8_product(torch.empty((0, K), dtype=x, device=DEV), w, s, index=index, out=out)
+    assert bool((out == 0).all())
+    # and beside rows that are there
+    c = make(R, K, N, 1, K, x="bf16" if x == torch.bfloat16 else "f32", tokens=2)
+    c["index"] = index
+    check(c, call(c, out_dtype=torch.float32))
+
+
 def test_many_experts():
     n = 1000
     rows = [(e * 7) % 5 for e in range(n)]
