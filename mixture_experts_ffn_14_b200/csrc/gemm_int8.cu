@@ -373,7 +373,17 @@ __global__ void __launch_bounds__(kPrepCta, 1)
       top_bits = __reduce_max_sync(0xffffffffu, lane < WARPS ? part[group][flip][lane] : 0u);
     }
     if (!ok) {
-      if (tid == 0) atomicOr(p.status, kStatusProducerTimeout);
+      if (tid == 0) {
+        atomicOr(p.status, kStatusProducerTimeout);
+        // unwinding: no copy may still be on its way into this CTA's memory
+        for (int i = 0; i < ring && r + i * step < p.R; ++i) {
+          mbar_wait(&full[group][slot], phase, kWaitLimitNs);
+          if (++slot == ring) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
       return;
     }
     // the row is in registers: its slot takes the next one
