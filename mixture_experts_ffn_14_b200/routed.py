@@ -50,7 +50,9 @@ def _on(stream, t, call, args):
 
     if not t.is_cuda:
         raise ValueError("moe: tensors must live on a CUDA device")
-    s = torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream
+    s = stream
+    if isinstance(stream, int):  # ExternalStream(0) would be a new stream, not the default one
+        s = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
     if s.device != t.device:
         raise ValueError(f"moe: stream is on {s.device}, the tensors on {t.device}")
     with torch.cuda.stream(s):

@@ -194,3 +194,30 @@ def test_nothing_is_written_outside_the_outputs():
     moe.moe_combine_topk(torch.ones((14, 72), device=DEV), torch.zeros((7, 2), dtype=torch.int32, device=DEV), out=out)
     torch.cuda.synchronize()
     assert intact([ob])
+
+
+def test_stream_given_as_a_handle():
+    # the handle's own stream is current during the call, 0 being the default stream
+    from mixture_experts_ffn_14_b200 import routed
+
+    x = torch.zeros((2, 8), device=DEV)
+    mine = torch.cuda.Stream()
+    handles = [0, mine.cuda_stream]
+    assert torch.cuda.default_stream().cuda_stream == 0
+    for other in (torch.cuda.default_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(other):
+            for h in handles:
+                assert routed._on(h, x, lambda: torch.cuda.current_stream().cuda_stream, ()) == h
+            assert torch.cuda.current_stream() == other
+    # work that is queued on the default stream comes before the call's
+    n = 1 << 24
+    big = torch.zeros(n, device=DEV)
+    logits = torch.zeros((64, 8), device=DEV)
+    mine.wait_stream(torch.cuda.default_stream())
+    for _ in range(50):
+        big.add_(1.0)
+    logits[:, 5] = big[n - 64:] / 25                  # 2.0 once all additions are done
+    with torch.cuda.stream(mine):
+        r = moe.moe_topk_route(logits, 1, stream=0)
+    torch.cuda.synchronize()
+    assert bool((r["idx"] == 5).all())
