@@ -369,6 +369,12 @@ template <int VPL>
 __device__ constexpr float key_slack() {
   return 1.2e-7f * VPL + 1.2e-7f;
 }
+// Below the normal range a step is 2^-149 whatever the value: what two keys may differ by
+// there, from the values they were made of, is at most this.
+template <int VPL>
+__device__ constexpr float key_floor() {
+  return VPL * 0x1p-148f;
+}
 
 // The same from 64-bit values, for groups that are runs of lanes: every lane scores those
 // of its experts again that may be one of the group's two largest (a, b: the group's two
@@ -381,7 +387,7 @@ __device__ __noinline__ unsigned settle_groups(const TopkParams& p, int64_t t, i
   float limit = -INFINITY;
   if (least >= kFirstKey) {
     const float v = bare_value<VPL>(least);
-    limit = v - 2.0f * err - 3.0f * key_slack<VPL>() * fabsf(v);
+    limit = v - 2.0f * err - 3.0f * key_slack<VPL>() * fabsf(v) - key_floor<VPL>();
   }
   const ExactRow row = by_score ? exact_row<BF16, VPL>(p, t, lane) : ExactRow{};
   const int e0 = lane_experts<VPL>(p, lane).first;
@@ -494,7 +500,7 @@ __device__ __forceinline__ unsigned kept_groups(const TopkParams& p, int64_t t, 
     const float low = __shfl_sync(kFull, mine, src), high = __shfl_sync(kFull, mine, next);
     const float sizes = __shfl_sync(kFull, size, src) + __shfl_sync(kFull, size, next);
     // an empty group is exact
-    if (high != -INFINITY && !(low - high > 4.0f * err + key_slack<VPL>() * sizes)) {
+    if (high != -INFINITY && !(low - high > 4.0f * err + key_slack<VPL>() * sizes + 2.0f * key_floor<VPL>())) {
       if (p.lane_run == 0 || !(sizes < INFINITY)) undecided = true;
       else kept = settle_groups<BF16, VPL>(p, t, lane, key, by_score, err, a, b);
     }
@@ -543,7 +549,7 @@ __device__ __forceinline__ void take_k(const TopkParams& p, int64_t t, uint32_t 
   // Two neighbours closer than both may be off (infinite values are close to everything).
   auto near = [&](uint32_t hi, uint32_t lo) {
     const float a = key_value(hi), b = key_value(lo);
-    return lo >= kFirstKey && !(a - b > 2.0f * err + key_slack<VPL>() * (fabsf(a) + fabsf(b)));
+    return lo >= kFirstKey && !(a - b > 2.0f * err + key_slack<VPL>() * (fabsf(a) + fabsf(b)) + key_floor<VPL>());
   };
   auto round = [&](int i) {
     // the values alone decide; among equal ones the lowest lane, in it the lowest register

@@ -153,6 +153,25 @@ def test_route_ties_and_near_ties_go_by_64_bits(kind, dtype):
     run_and_check(l, k, kind, bias=bias, groups=16, keep=5, rule="max", renorm=True)
 
 
+@pytest.mark.parametrize("E", [33, 64, 96, 128, 256, 512, 1000])
+@pytest.mark.parametrize("span", [3, 40, 3000, 1 << 24])
+def test_route_logits_below_the_normal_range(E, span):
+    # multiples of 2^-149 of either sign, and at the largest span normal numbers beside them: there a
+    # key's lost bits are steps of a fixed size
+    steps = torch.randint(-span, span + 1, (60, E), generator=gen(E + span), device=DEV, dtype=torch.int32)
+    l = torch.where(steps < 0, -1.0, 1.0) * steps.abs().view(torch.float32)
+    assert torch.equal((l.double() * 2.0 ** 149).abs()[steps.abs() < 1 << 23].long(), steps.abs()[steps.abs() < 1 << 23].long())
+    l[0] = -1.0
+    l[0, 0], l[0, 1] = 2.0 ** -148, 2.0 ** -148 + 2.0 ** -149
+    run_and_check(l, 1, "softmax")
+    run_and_check(l, 8, "sigmoid", renorm=True)
+    for groups in (2, 8, 3):
+        if E % groups == 0:
+            run_and_check(l, 4, "softmax", groups=groups, keep=1, rule="max")
+            run_and_check(l, 4, "softmax", groups=groups, keep=groups - 1, rule="max")
+            run_and_check(l, 4, "sigmoid", groups=groups, keep=groups - 1, rule="top2")
+
+
 @pytest.mark.parametrize("n", [0, 1, 37, 64, 100, 500, -3])
 @pytest.mark.parametrize("T", [20, 100])
 def test_route_padded_batch(T, n):
