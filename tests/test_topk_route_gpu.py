@@ -172,6 +172,27 @@ def test_route_logits_below_the_normal_range(E, span):
             run_and_check(l, 4, "sigmoid", groups=groups, keep=groups - 1, rule="top2")
 
 
+@pytest.mark.parametrize("E,groups", [(16, 4), (96, 8), (96, 3), (256, 8), (1000, 10)])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_groups_whose_sum_of_two_leaves_the_fp32_range(E, groups, kind):
+    # biases of the type's lowest and largest value: a group that sums to -2^129 is still above
+    # one that has no expert left
+    l = torch.randn((12 * groups, E), generator=gen(E), device=DEV)
+    size = E // groups
+    low, top = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    for t in range(l.shape[0]):
+        g = t % groups
+        l[t, :g * size] = -float("inf")              # the first groups have nothing left
+        if t >= 6 * groups:
+            l[t, (groups - 1) * size:] = -float("inf")
+    mixed = torch.where(torch.arange(E, device=DEV) % 3 == 0, low, 0.0)
+    ends = torch.where(torch.arange(E, device=DEV) % 5 == 0, top, low)
+    for bias in (torch.full((E,), low, device=DEV), torch.full((E,), top, device=DEV), mixed, ends, ends * 0.6):
+        for keep in (1, groups - 1):
+            run_and_check(l, 2, kind, bias=bias, groups=groups, keep=keep, rule="top2")
+            run_and_check(l, 2, kind, bias=bias, groups=groups, keep=keep, rule="max")
+
+
 @pytest.mark.parametrize("n", [0, 1, 37, 64, 100, 500, -3])
 @pytest.mark.parametrize("T", [20, 100])
 def test_route_padded_batch(T, n):
