@@ -469,7 +469,8 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // accuracy of large negative z (1 + tanh would cancel), and is two special-function
 // instructions. The mode is looked at once for all of them.
 //   GELU (tanh form) = z / (1 + e^-t), t = 2 sqrt(2 / pi) (z + 0.044715 z^3); SiLU: t = z
-// (z c3) z, not z^2 c3: with c3 = 0 a z^2 past the fp32 range would make NaN of it.
+// SiLU has no cubic term at all: one with a factor of 0 would make NaN of 0 * inf, where z
+// is +inf or its square leaves the fp32 range. A z of -inf is NaN in every mode (-inf * 0).
 template <int N>
 __device__ __forceinline__ void activate(float (&z)[N], int mode) {
   constexpr float kLog2e = 1.4426950408889634f;
@@ -477,9 +478,11 @@ __device__ __forceinline__ void activate(float (&z)[N], int mode) {
   if (mode == MOE_ACT_GELU_ERF) {
 #pragma unroll
     for (int j = 0; j < N; ++j) z[j] *= 0.5f * erfcf(-0.70710678118654752f * z[j]);
+  } else if (mode == MOE_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) z[j] *= rcp_fast(1.0f + ex2_fast(-kLog2e * z[j]));
   } else {
-    const float c1 = mode == MOE_ACT_SILU ? -kLog2e : -kLog2e * kTanh;
-    const float c3 = mode == MOE_ACT_SILU ? 0.0f : -kLog2e * kTanh * 0.044715f;
+    constexpr float c1 = -kLog2e * kTanh, c3 = c1 * 0.044715f;
 #pragma unroll
     for (int j = 0; j < N; ++j) z[j] *= rcp_fast(1.0f + ex2_fast(z[j] * fmaf(z[j] * c3, z[j], c1)));
   }

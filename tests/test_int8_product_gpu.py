@@ -159,6 +159,25 @@ def test_gate_values_whose_square_leaves_the_fp32_range(R, n, act):
         assert bool((err[sure] <= 12 * U * want.abs()[sure]).all()) and not bool(torch.isnan(got[r]).any())
 
 
+@pytest.mark.parametrize("act", ["gelu", "erf", "silu"])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["obf16", "of32"])
+@pytest.mark.parametrize("R,N", [(40, 16), (40, 4112), (110, 20000), (700, 272), (1400, 4112)])
+def test_gate_values_of_infinity(R, N, out, act):
+    # act(+inf) = +inf, act(-inf) = -inf * 0, a NaN, times an up value of 127 * 64 * 1e-36 * 1e38 (8e5)
+    K = 64
+    x = torch.full((R, K), 1e38, device=DEV)
+    x[1::2] *= -1
+    w = torch.full((1, K, N), 127, dtype=torch.int8, device=DEV)
+    w[:, :, 3::4] = -127
+    s = torch.full((1, N), 1e4, device=DEV, dtype=torch.bfloat16)
+    su = torch.full((1, N), 1e-36, device=DEV, dtype=torch.bfloat16)
+    got = moe.moe_int8_product(x, w, s, w_up=w.abs(), s_up=su, activation=ACT[act], out_dtype=out)
+    z = x[:, :1] * w[0, :1]                          # its sign is the gate value's; the up value has the row's
+    assert torch.equal(torch.isnan(got), z < 0)
+    want = torch.where(x[:, :1] > 0, math.inf, -math.inf).expand(R, N)
+    assert torch.equal(got[z > 0].float(), want[z > 0])
+
+
 @pytest.mark.parametrize("R,rows", [(40, [5, 0, 7, 20]), (600, [200, 0, 100, 150])])
 def test_rows_behind_the_last_expert_stay(R, rows):
     c = make(R, 272, 144, 4, R, rows=rows, tokens=33)
