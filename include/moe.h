@@ -369,11 +369,12 @@ typedef struct {
   float* gate_perm;    /* [T*k]  weight of each permuted row, 0 behind the last one       */
 } moe_topk_routed_t;
 
-/* Workspace bytes of moe_topk_route: 0 when none is needed (no dispatch arrays
- * asked for, or a batch of one block) and on bad sizes. */
+/* Workspace bytes of moe_topk_route with the dispatch arrays: 0 when none is needed (up to
+ * 256 tokens; a call without the arrays needs none either) and on bad sizes. */
 MOE_EXPORT size_t moe_topk_workspace_size(int64_t T, int32_t E, int32_t k);
 
-/* See moe_topk_args_t. `workspace` may be NULL when the size above is 0. */
+/* See moe_topk_args_t. `workspace` may be NULL when none is needed; one that is given all
+ * the same (256-byte aligned, 4 bytes or more) gets its status word written. */
 MOE_EXPORT moe_status_t moe_topk_route(const moe_topk_args_t* args, const moe_topk_routed_t* routed,
                                        void* workspace, size_t ws_bytes, moe_stream_t stream);
 

@@ -51,7 +51,7 @@ struct TopkParams {
   int32_t* idx;
   float* weights;
   float* scores;
-  // dispatch (counts == nullptr: none); hist, totals and status with more than kClusterBlocks blocks
+  // dispatch (counts == nullptr: none); hist and totals with more than kClusterBlocks blocks
   int32_t* counts;
   int32_t* offsets;
   int32_t* perm_token;
@@ -61,7 +61,7 @@ struct TopkParams {
   int32_t* hist;    // [nblk, E] slots per token block, then their exclusive prefix over blocks
   int32_t* totals;  // [E]
   int64_t nblk;
-  uint32_t* status; // workspace status word: nothing here can fail, so it is set to 0
+  uint32_t* status; // status word of the workspace, if one is given: nothing here can fail, so it is set to 0
 };
 
 __device__ __forceinline__ int64_t token_count(const TopkParams& p) {
@@ -891,6 +891,7 @@ __global__ void __launch_bounds__(NW * 32, route_ctas(VPL, NW))
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTopkBlock;
   const int64_t n = token_count(p);
   const bool dispatch = p.counts != nullptr;
+  if (p.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   if (dispatch) {
     for (int e = threadIdx.x; e < p.E; e += NW * 32) mask[e] = 0;
     __syncthreads();
@@ -963,7 +964,6 @@ __global__ void __launch_bounds__(1024) moe_topk_scan_kernel(const TopkParams p)
   __shared__ int run[32][33];
   sm100::launch_dependents();
   sm100::wait_prerequisites();  // the blocks' histograms
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   const int x = threadIdx.x % 32, y = threadIdx.x / 32;
   const int e = blockIdx.x * 32 + x;
   const int64_t per = (p.nblk + 31) / 32, b0 = y * per, b1 = b0 + per < p.nblk ? b0 + per : p.nblk;
@@ -1278,8 +1278,9 @@ moe_status_t moe_topk_route(const moe_topk_args_t* a, const moe_topk_routed_t* r
   if (ws) {
     p.hist = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + L.hist);
     p.totals = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + L.totals);
-    p.status = static_cast<uint32_t*>(workspace);
   }
+  if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0 && ws_bytes >= sizeof(uint32_t))
+    p.status = static_cast<uint32_t*>(workspace);
   const unsigned grid = static_cast<unsigned>(L.nblk);
   const bool few = L.nblk <= device_sm_count();
   const bool cluster = dispatch && L.nblk > 1 && L.nblk <= kClusterBlocks;

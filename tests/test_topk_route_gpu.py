@@ -226,6 +226,21 @@ def test_route_without_dispatch_and_with_given_outputs():
         moe.moe_topk_route(l, 65)
 
 
+@pytest.mark.parametrize("T,dispatch", [(1, True), (40, True), (256, True), (300, True), (300, False), (6000, False)])
+def test_route_writes_the_status_word_of_a_given_workspace(T, dispatch):
+    l = logits_of(T, 64, torch.float32, 6)
+    ws = torch.full((moe.moe_topk_workspace_size(T, 64, 4) or 256,), 0x40, dtype=torch.uint8, device=DEV)
+    assert moe.moe_device_status(ws) == (6, 0x40404040)
+    moe.moe_topk_route(l, 4, workspace=ws, dispatch=dispatch)
+    assert moe.moe_device_status(ws) == (0, 0)
+    if T <= 256 or not dispatch:                    # nothing else of it is used
+        assert bool((ws[4:] == 0x40).all())
+        for start, end in ((1, 200), (0, 3), (0, 0)):   # no status word fits there: left alone
+            ws.fill_(0x40)
+            moe.moe_topk_route(l, 4, workspace=ws[start:end], dispatch=dispatch)
+            assert bool((ws == 0x40).all())
+
+
 def test_route_empty_batch():
     l = torch.empty((0, 16), device=DEV)
     r = moe.moe_topk_route(l, 2)
