@@ -173,7 +173,10 @@ struct Result {
   Result(PyObject* given, const char* name, at::IntArrayRef shape, at::ScalarType t, at::Device dev, bool zeros = false)
       : type(t) {
     if (given != nullptr && given != Py_None) {
-      at = need(given, name, shape, t, dev).mutable_data_ptr();
+      const at::Tensor& out = need(given, name, shape, t, dev);
+      at = out.mutable_data_ptr();
+      // what autograd has saved of it is no longer what it was
+      if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
       object = Py_NewRef(given);
     } else {
       at::Tensor made = empty(shape, t, dev);

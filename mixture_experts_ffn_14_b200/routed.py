@@ -5,7 +5,11 @@ Every tensor is dense, on one CUDA device, which need not be the current one;
 the work goes to ``stream`` (a torch stream or a handle), by default that
 device's current stream. Outputs and workspaces that are not given are allocated
 on that stream. Wrong shapes, types and devices raise ``ValueError``, a call that
-the library refuses ``MoeError``; nothing is launched in either case.
+the library refuses ``MoeError``; no kernel of the library is launched in either case.
+
+The calls are no part of an autograd graph: their results require no gradient, whatever
+their inputs do (the weights' and scores' gradient is moe_topk_route_backward). A tensor
+given as an output counts as changed in place for autograd.
 
     r = moe.moe_topk_route(logits, 8, score=moe.MOE_SCORE_SIGMOID, bias=bias, renormalize=True)
     ...                                  # experts on rows r["perm_token"], gates r["gate_perm"]

@@ -221,3 +221,37 @@ def test_stream_given_as_a_handle():
         r = moe.moe_topk_route(logits, 1, stream=0)
     torch.cuda.synchronize()
     assert bool((r["idx"] == 5).all())
+
+
+def test_given_outputs_count_as_changed_in_place():
+    T, E, k, d = 40, 16, 2, 64
+    l, y = torch.randn((T, E), device=DEV), torch.randn((T * k, d), device=DEV)
+    w, s = torch.ones((1, d, 32), dtype=torch.int8, device=DEV), torch.ones((1, 32), dtype=torch.bfloat16, device=DEV)
+    outs = {n: torch.zeros_like(t) for n, t in moe.moe_topk_route(l, k, want_scores=True).items()}
+    idx, gw = outs["idx"], torch.zeros((T, k), device=DEV)
+    grad, comb, prod = torch.zeros_like(l), torch.zeros((T, d), device=DEV), torch.zeros((T * k, 32), device=DEV)
+    calls = [(list(outs.values()), lambda: moe.moe_topk_route(l, k, want_scores=True, out=outs)),
+             ([grad], lambda: moe.moe_topk_route_backward(l, idx, gw, out=grad)),
+             ([comb], lambda: moe.moe_combine_topk(y, outs["slot_pos"], out=comb)),
+             ([prod], lambda: moe.moe_int8_product(y, w, s, out=prod))]
+    for given, run in calls:
+        before, same = [t._version for t in given], [t._version for t in (l, y, gw, w, s)]
+        run()
+        assert all(t._version > v for t, v in zip(given, before))
+        assert same == [t._version for t in (l, y, gw, w, s)]
+    # a value that autograd has kept is not read once it is overwritten
+    p = torch.ones((T, d), device=DEV, requires_grad=True)
+    loss = (p * comb).sum()
+    moe.moe_combine_topk(y, outs["slot_pos"], out=comb)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():                       # tensors without a version
+        kept = torch.zeros((T, d), device=DEV)
+        assert torch.equal(moe.moe_combine_topk(y, outs["slot_pos"], out=kept), comb)
+
+
+def test_results_are_no_part_of_an_autograd_graph():
+    l = torch.randn((8, 16), device=DEV, requires_grad=True)
+    r = moe.moe_topk_route(l, 2, want_scores=True)
+    assert not any(t.requires_grad for t in r.values())
+    assert not moe.moe_topk_route_backward(l, r["idx"], torch.ones((8, 2), device=DEV)).requires_grad
