@@ -11,13 +11,15 @@ status bit 0x40 and skips the access. Load it with
 ``MOE_B200_LIBRARY=libmoe_b200_debug.so``.
 
 ``build_torch_calls`` compiles ``_torch_calls.so`` (csrc/torch_calls.cpp), the binding of
-the routing, combine and int8 calls, against the installed torch's headers.
+the routing, combine and int8 calls, against the installed torch's headers; again when
+torch or Python is another one than it was compiled for.
 """
 
 from __future__ import annotations
 
 import argparse
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -33,6 +35,7 @@ LIB = os.path.join(PKG, "libmoe_b200.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libmoe_b200_debug.so")
 TORCH_CALLS = os.path.join(PKG, "_torch_calls.so")
+TORCH_CALLS_TAG = os.path.join(BUILD, "torch_calls.tag")  # torch and Python that it was compiled for
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + [
@@ -82,13 +85,21 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
     return lib
 
 
+def _torch_tag() -> str:
+    return f"torch {importlib.metadata.version('torch')}, {sysconfig.get_config_var('SOABI')}"
+
+
 def build_torch_calls(force: bool = False, verbose: bool = False) -> str:
     src = os.path.join(CSRC, "torch_calls.cpp")
-    if not force and not _stale(TORCH_CALLS, [src] + _headers()):
-        return TORCH_CALLS
+    built_for = ""
+    if os.path.exists(TORCH_CALLS_TAG):
+        with open(TORCH_CALLS_TAG) as f:
+            built_for = f.read().strip()
     spec = importlib.util.find_spec("torch")
     if spec is None:
         raise RuntimeError("torch not found: its headers are required to build _torch_calls.so")
+    if not force and built_for == _torch_tag() and not _stale(TORCH_CALLS, [src] + _headers()):
+        return TORCH_CALLS
     import torch
 
     home = os.path.dirname(spec.origin)
@@ -103,6 +114,9 @@ def build_torch_calls(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
+    os.makedirs(os.path.dirname(TORCH_CALLS_TAG), exist_ok=True)
+    with open(TORCH_CALLS_TAG, "w") as f:
+        f.write(_torch_tag() + "\n")
     return TORCH_CALLS
 
 
