@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import mixture_experts_ffn_14_b200 as moe
+from _int8_plan import CASES, form
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -128,6 +129,20 @@ def test_tiles_of_several_ctas(R, N, rows, K, pair):
     outs = [call(c, workspace=ws) for _ in range(3)]      # one workspace, one call after the other
     check(c, outs[0])
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("x,out", [("bf16", torch.bfloat16), ("f32", torch.float32), ("i8", torch.float32)])
+@pytest.mark.parametrize("name,tile,R,K,N,rows,pair", CASES,
+                         ids=[f"{c[0]}{c[1]}-{c[2]}x{c[3]}x{c[4]}-{'gated' if c[6] else 'plain'}" for c in CASES])
+def test_every_form(name, tile, R, K, N, rows, pair, x, out):
+    assert form(R, K, N, len(rows), x, pair)[:2] == (name, tile)
+    c = make(R, K, N, len(rows), R + K + N + len(rows), x=x, pair=pair, rows=rows, gate=True)
+    o = torch.full((R, N), 7.0, device=DEV, dtype=out)
+    first = call(c, out=o).clone()
+    check(c, o, tail=7.0)
+    # the sums are integers: whatever order the tiles and their parts come in, the same bits
+    for _ in range(3):
+        assert torch.equal(call(c, out=o.fill_(7.0)), first)
 
 
 @pytest.mark.parametrize("act", ["gelu", "erf", "silu"])
