@@ -7,6 +7,7 @@ import math
 import pytest
 import torch
 
+import _routed_reference as ref
 import mixture_experts_ffn_14_b200 as moe
 from _int8_plan import CASES, form
 
@@ -402,3 +403,69 @@ def test_one_layer_of_the_operators_together(T, d, f, E, k, kind):
             # independent, so their root mean square counts, with a factor 8 for the largest of all
             size[t] += float(r["weights"][t, j]) * (xt.abs().max() / 254 * 2 + hh.abs().max() / 254)
         assert bool(((out[t].double() - want[t]).abs() <= 8 * size[t] + want[t].abs() * 2.0 ** -8).all())
+
+
+def failing(c, got):
+    """Share of the elements of the result that check() would refuse."""
+    want, lim = reference(c)
+    half = 0 if got.dtype == torch.float32 else torch.finfo(got.dtype).eps / 2
+    err = (got[:want.shape[0]].double() - want).abs()
+    return float((err > lim * 1.01 + half * (want.abs() + lim) + 1e-36).double().mean())
+
+
+@pytest.mark.parametrize("T,d,f,E,k,kind", [(1, 256, 384, 8, 2, "softmax"), (50, 256, 384, 8, 2, "softmax"),
+                                            (300, 512, 256, 24, 6, "sigmoid"), (700, 256, 640, 16, 3, "sigmoid")])
+def test_one_layer_against_a_choice_and_an_order_made_in_64_bits(T, d, f, E, k, kind):
+    """The same layer, every step against its 64-bit value from what the step before it
+    left, but at the experts, weights and places of a routing in 64 bits, not of the call's own
+    arrays: a row at another place, of another token, expert or slot is refused."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T + 1)
+    x = torch.randn((T, d), generator=g, device=DEV).to(torch.bfloat16)
+    logits = torch.randn((T, E), generator=g, device=DEV)
+    i8 = lambda *s: torch.randint(-127, 128, s, generator=g, device=DEV, dtype=torch.int8)  # noqa: E731
+    sc = lambda n, m, fan: ((torch.rand((n, m), generator=g, device=DEV) + 0.5) / (127 * math.sqrt(fan))).to(torch.bfloat16)  # noqa: E731
+    wg, wu, wd = i8(E, d, f), i8(E, d, f), i8(E, f, d)
+    sg, su, sd = sc(E, f, d), sc(E, f, d), sc(E, d, f)
+    n = T - T // 5
+    r = moe.moe_topk_route(logits, k, score=moe.MOE_SCORE_SIGMOID if kind == "sigmoid" else moe.MOE_SCORE_SOFTMAX,
+                           renormalize=True, n_tokens=torch.tensor([n], dtype=torch.int32, device=DEV))
+    h = moe.moe_int8_product(x, wg, sg, index=r["perm_token"], counts=r["counts"], w_up=wu, s_up=su)
+    y = moe.moe_int8_product(h, wd, sd, counts=r["counts"], gate=r["gate_perm"], out_dtype=torch.float32)
+    out = moe.moe_combine_topk(y, r["slot_pos"], out_dtype=torch.bfloat16)
+
+    want = ref.route(logits.double().cpu().numpy(), k, kind, renorm=True, n=n)
+    # the weights: 20 roundings and two for each unit that a row's logits span (below 12 here)
+    w = r["weights"].double().cpu().numpy()
+    assert (abs(w - want["weights"]) <= 44 * U * want["weights"]).all()
+    rows, m = want["counts"].tolist(), n * k
+    token, slot = (torch.from_numpy(want[name]).to(DEV) for name in ("perm_token", "perm_slot"))
+    gate = torch.zeros(T * k, device=DEV)
+    gate[:m] = r["weights"][token[:m], slot[:m]]
+    up = {"x": x, "x_scale": None, "index": token.int(), "rows": rows, "w": wg, "s": sg, "w_up": wu, "s_up": su,
+          "gate": None}
+    down = {"x": h, "x_scale": None, "index": None, "rows": rows, "w": wd, "s": sd, "w_up": None, "s_up": None,
+            "gate": gate}
+    check(up, h, tail=0.0)
+    check(down, y, tail=0.0)
+    pos = torch.from_numpy(want["slot_pos"]).to(DEV)
+
+    def combined(pos):
+        part = torch.where((pos >= 0)[:, :, None], y.double()[pos.clamp(min=0)], 0.0)
+        total = part.sum(1)
+        # k additions, then the rounding to 16 bits
+        return total, 2 * k * U * part.abs().sum(1) + 2.0 ** -8 * 1.01 * total.abs() + 1e-37
+
+    total, lim = combined(pos)
+    assert bool(((out.double() - total).abs() <= lim).all()) and bool((out[n:] == 0).all())
+    # what these bounds refuse: nothing at all, and each kind of exchange
+    assert float((total[:n].abs() > lim[:n]).double().mean()) > 0.99
+    assert failing(up, torch.zeros_like(h)) > 0.9 and failing(down, torch.zeros_like(y)) > 0.9
+    if n > 1:
+        assert failing({**up, "index": token.int().roll(1)}, h) > 0.9
+        other, lim = combined(torch.cat([pos[:n].roll(1, 0), pos[n:]]))
+        assert float(((out.double() - other).abs() > lim)[:n].double().mean()) > 0.9
+        swapped = torch.zeros_like(gate)
+        swapped[:m] = r["weights"].roll(1, 1)[token[:m], slot[:m]]
+        assert failing({**down, "gate": swapped}, y) > 0.9
+        assert failing({**down, "w": wd.roll(1, 0)}, y) > 0.9
