@@ -369,11 +369,11 @@ template <int VPL>
 __device__ constexpr float key_slack() {
   return 1.2e-7f * VPL + 1.2e-7f;
 }
-// Below the normal range a step is 2^-149 whatever the value: what two keys may differ by
-// there, from the values they were made of, is at most this.
+// Below the normal range a step is 2^-149 whatever the value and the slack rounds to nothing:
+// what a key is off by there, as a value's own error (comparisons take it twice or more).
 template <int VPL>
 __device__ constexpr float key_floor() {
-  return VPL * 0x1p-148f;
+  return VPL * 0x1p-149f;
 }
 
 // The same from 64-bit values, for groups that are runs of lanes: every lane scores those
@@ -387,7 +387,7 @@ __device__ __noinline__ unsigned settle_groups(const TopkParams& p, int64_t t, i
   float limit = -INFINITY;
   if (least >= kFirstKey) {
     const float v = bare_value<VPL>(least);
-    limit = v - 2.0f * err - 3.0f * key_slack<VPL>() * fabsf(v) - key_floor<VPL>();
+    limit = v - 2.0f * err - 3.0f * key_slack<VPL>() * fabsf(v);
   }
   const ExactRow row = by_score ? exact_row<BF16, VPL>(p, t, lane) : ExactRow{};
   const int e0 = lane_experts<VPL>(p, lane).first;
@@ -502,7 +502,7 @@ __device__ __forceinline__ unsigned kept_groups(const TopkParams& p, int64_t t, 
     const float low = __shfl_sync(kFull, mine, src), high = __shfl_sync(kFull, mine, next);
     const float sizes = __shfl_sync(kFull, size, src) + __shfl_sync(kFull, size, next);
     // an empty group is exact
-    if (high != -INFINITY && !(low - high > 4.0f * err + key_slack<VPL>() * sizes + 2.0f * key_floor<VPL>())) {
+    if (high != -INFINITY && !(low - high > 4.0f * err + key_slack<VPL>() * sizes)) {
       if (p.lane_run == 0 || !(sizes < INFINITY)) undecided = true;
       else kept = settle_groups<BF16, VPL>(p, t, lane, key, by_score, err, a, b);
     }
@@ -551,7 +551,7 @@ __device__ __forceinline__ void take_k(const TopkParams& p, int64_t t, uint32_t 
   // Two neighbours closer than both may be off (infinite values are close to everything).
   auto near = [&](uint32_t hi, uint32_t lo) {
     const float a = key_value(hi), b = key_value(lo);
-    return lo >= kFirstKey && !(a - b > 2.0f * err + key_slack<VPL>() * (fabsf(a) + fabsf(b)) + key_floor<VPL>());
+    return lo >= kFirstKey && !(a - b > 2.0f * err + key_slack<VPL>() * (fabsf(a) + fabsf(b)));
   };
   auto round = [&](int i) {
     // the values alone decide; among equal ones the lowest lane, in it the lowest register
@@ -776,7 +776,7 @@ __device__ __forceinline__ int choose(const TopkParams& p, int64_t t, int lane, 
     }
     if (VPL <= 8) sort_keys<VPL>(key);
     // exact where no logit has a bit that the index took
-    err = VPL > 1 && __any_sync(kFull, (lost & (VPL - 1)) != 0) ? 0.0f : -1.0f;
+    err = VPL > 1 && __any_sync(kFull, (lost & (VPL - 1)) != 0) ? key_floor<VPL>() : -1.0f;
   }
   if (groups && !(sums && !biased)) kept = kept_groups<BF16, VPL>(p, t, lane, key, biased, err, undecided);
   if (groups && p.lane_run > 0) {
