@@ -480,13 +480,12 @@ __device__ __forceinline__ unsigned kept_groups(const TopkParams& p, int64_t t, 
     size = fabsf(mine);
     if (sum && b >= kFirstKey) {
       const float second = bare_value<VPL>(b);
-      mine += second;
+      // a sum that leaves the fp32 range to -inf would tie with an empty group; its size is
+      // infinite, so that the limit next to it is decided in 64 bits
+      mine = fmaxf(mine + second, -FLT_MAX);
       size += fabsf(second);
     }
   }
-  // infinite biases, or a sum of two that leaves the fp32 range (to -inf it would tie with an
-  // empty group)
-  if (__any_sync(kFull, leader && (mine != mine || (a >= kFirstKey && mine == -INFINITY)))) undecided = true;
   // largest first, the lower group among equal ones; + 1: an empty group is above no group
   uint32_t left = leader ? order_key(mine) + 1 : 0;
   unsigned kept = 0;
