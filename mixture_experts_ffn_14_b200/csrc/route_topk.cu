@@ -890,7 +890,6 @@ __global__ void __launch_bounds__(NW * 32, route_ctas(VPL, NW))
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTopkBlock;
   const int64_t n = token_count(p);
   const bool dispatch = p.counts != nullptr;
-  if (p.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   if (dispatch) {
     for (int e = threadIdx.x; e < p.E; e += NW * 32) mask[e] = 0;
     __syncthreads();
@@ -929,6 +928,7 @@ __global__ void __launch_bounds__(NW * 32, route_ctas(VPL, NW))
       p.weights[t * p.k + slot] = w * p.scale;
     }
   }
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.status != nullptr) *p.status = 0;
   if (!dispatch) return;
   if (p.nblk > kClusterBlocks) {
     for (int e = threadIdx.x; e < p.E; e += NW * 32)
