@@ -711,12 +711,16 @@ __device__ __noinline__ int choose_exact(const TopkParams& p, int64_t t, int lan
 // Share of each choice in the renormalised weights (P lanes of a warp, a power of two,
 // hold the choices of one token; logit lv, -inf = none): s / sum s, computed from
 // differences of logits, so that scores below the fp32 range still share. Sigmoid
-// scores of logits below -60 are exp(l) to 26 digits.
+// scores e^l / (1 + e^l) over e^top, unless the largest logit is positive: then the largest
+// score is above a half, and scores below the fp32 range have no share in it.
 __device__ __forceinline__ float share_of(int score, float lv, int P) {
   float top = lv;
   for (int o = 1; o < P; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
   float x = 0.0f;
-  if (lv > -INFINITY) x = score == MOE_SCORE_SIGMOID && top > -60.0f ? sigmoid(lv) : expf(lv - top);
+  if (lv > -INFINITY) {
+    if (score == MOE_SCORE_SIGMOID && top > 0.0f) x = sigmoid(lv);
+    else x = expf(lv - top) / (score == MOE_SCORE_SIGMOID ? 1.0f + expf(lv) : 1.0f);
+  }
   float sum = x;
   for (int o = 1; o < P; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
   return sum > 0.0f ? x / sum : 0.0f;

@@ -172,6 +172,21 @@ def test_route_logits_below_the_normal_range(E, span):
             run_and_check(l, 4, "sigmoid", groups=groups, keep=groups - 1, rule="top2")
 
 
+@pytest.mark.parametrize("mean", [-100.0, -80.0, -60.0, -40.0, 0.0, 60.0])
+@pytest.mark.parametrize("E,k", [(3, 3), (24, 24), (256, 8)])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_shares_of_scores_far_below_the_largest(mean, E, k, kind):
+    # chosen scores out to e^-60 of the largest, on either side of the fp32 range
+    l = mean + 15.0 * torch.randn((64, E), generator=gen(E), device=DEV)
+    run_and_check(l, k, kind, renorm=True)
+    run_and_check(l, k, kind, renorm=True, bias=torch.randn(E, generator=gen(3), device=DEV))
+    idx = moe.moe_topk_route(l, k, score=SCORE[kind], dispatch=False)["idx"]
+    gw = torch.randn((64, k), generator=gen(4), device=DEV)
+    got = moe.moe_topk_route_backward(l, idx, gw, score=SCORE[kind], renormalize=True)
+    a = (l.double().cpu().numpy(), idx.cpu().numpy(), gw.double().cpu().numpy(), kind, True, 1.0)
+    assert (np.abs(got.double().cpu().numpy() - ref.route_backward(*a)) <= grad_bound(*a, None, 64)).all()
+
+
 @pytest.mark.parametrize("E,groups", [(16, 4), (96, 8), (96, 3), (256, 8), (1000, 10)])
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 def test_route_groups_whose_sum_of_two_leaves_the_fp32_range(E, groups, kind):
