@@ -387,7 +387,7 @@ __device__ __noinline__ unsigned settle_groups(const TopkParams& p, int64_t t, i
   float limit = -INFINITY;
   if (least >= kFirstKey) {
     const float v = bare_value<VPL>(least);
-    limit = v - 2.0f * err - 3.0f * key_slack<VPL>() * fabsf(v);
+    limit = v < INFINITY ? v - 2.0f * err - 3.0f * key_slack<VPL>() * fabsf(v) : v;
   }
   const ExactRow row = by_score ? exact_row<BF16, VPL>(p, t, lane) : ExactRow{};
   const int e0 = lane_experts<VPL>(p, lane).first;

@@ -187,6 +187,21 @@ def test_route_shares_of_scores_far_below_the_largest(mean, E, k, kind):
     assert (np.abs(got.double().cpu().numpy() - ref.route_backward(*a)) <= grad_bound(*a, None, 64)).all()
 
 
+@pytest.mark.parametrize("E,groups", [(64, 8), (224, 7), (256, 8), (512, 16), (1000, 10), (96, 3)])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_infinite_biases_beside_a_near_tie_of_groups(E, groups, kind):
+    # the groups at the limit are equal in 32 bits, those far above it hold a bias of +inf
+    l = 1.0 + torch.randint(-3, 4, (64, E), generator=gen(E), device=DEV) * 2.0 ** -23
+    l[torch.rand((64, E), generator=gen(E + 1), device=DEV) < 0.5] = float("nan")
+    bias = torch.randint(-1, 2, (E,), generator=gen(E + 2), device=DEV).float()
+    for g in range(0, groups, 3):
+        bias[g * (E // groups) + 1:(g + 1) * (E // groups):2] = float("inf")
+    bias[E // 2] = -float("inf")
+    for keep in range(1, groups):
+        for rule in ("max", "top2"):
+            run_and_check(l, 5, kind, bias=bias, groups=groups, keep=keep, rule=rule, renorm=True)
+
+
 @pytest.mark.parametrize("E,groups", [(16, 4), (96, 8), (96, 3), (256, 8), (1000, 10)])
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 def test_route_groups_whose_sum_of_two_leaves_the_fp32_range(E, groups, kind):
