@@ -51,7 +51,9 @@
  *                           left the fp16 range (|v| > 65504 became infinite);
  *                           the output is not valid
  *   0x40                    library built with MOE_DEBUG_BOUNDS: an index
- *                           outside its array was caught and the access skipped
+ *                           outside its array was caught and the access skipped;
+ *                           moe_int8_product in every build: counts that leave
+ *                           [0, R] were cut off
  * Behaviour on non-finite inputs is unspecified.
  */
 #ifndef MOE_B200_MOE_H
@@ -315,7 +317,8 @@ MOE_EXPORT moe_status_t moe_gather_rows(const void* src, int64_t src_rows, const
  * and give the router's gradient for training. They follow the file header's rules
  * (dense, row-major, 16-byte aligned device arrays; checks on the host; no
  * synchronisation; nothing kept between calls); calls that may overlap on the
- * GPU need distinct workspaces and outputs. */
+ * GPU need distinct workspaces and outputs. Outputs overlap neither one another
+ * nor an input, except where a call says so. */
 
 typedef enum {
   MOE_SCORE_SOFTMAX = 0, /* s = softmax(logits) over the E experts */
@@ -334,7 +337,7 @@ typedef enum {
  *   with n_groups > 1 the E experts form n_groups runs of E / n_groups, and only
  *   the topk_groups groups of the largest value stay (ties: the lower group);
  *   idx = the k largest c in descending order, ties to the lower expert;
- *   weights = scale * s[idx], divided by their sum if renormalize == 1.
+ *   weights = scale * s[idx], divided by the sum of s[idx] if renormalize == 1.
  * The bias steers the choice only. The choice is that of the values in 64 bits:
  * where 32 bits cannot decide, the kernel decides in 64. A token with fewer than
  * k experts to choose from gets idx -1 and weight 0 in the slots left over.
@@ -499,8 +502,11 @@ MOE_EXPORT int32_t moe_abi_version(void);
 
 /* No counterpart on the pages. Options the library was compiled with, as bits:
  * MOE_BUILD_DEBUG_BOUNDS = the MOE_DEBUG_BOUNDS build (every index that one
- * kernel computes and another uses is checked before the access; a failed
- * check sets status bit 0x40 and skips the access; slower, for testing). */
+ * kernel of the sublayer or of its expert-parallel pieces computes and another
+ * uses is checked before the access; a failed check sets status bit 0x40 and
+ * skips the access; slower, for testing). The kernels of the calls of any E and
+ * k hold no such checks; indices and counts that a caller gives them are bounded
+ * in every build. */
 #define MOE_BUILD_DEBUG_BOUNDS 1
 MOE_EXPORT int32_t moe_build_flags(void);
 

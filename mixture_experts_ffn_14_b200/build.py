@@ -5,9 +5,11 @@ Objects go to ``mixture_experts_ffn_14_b200/_build/`` and are rebuilt when a
 source or header is newer than the object. Cross-compiles without a GPU.
 
 ``--debug-bounds`` builds ``libmoe_b200_debug.so`` from the same sources with
-``-DMOE_DEBUG_BOUNDS`` (objects in ``_build_debug/``): every index one kernel
-computes and another uses is checked before the access, a failed check sets
-status bit 0x40 and skips the access. Load it with
+``-DMOE_DEBUG_BOUNDS`` (objects in ``_build_debug/``): every index that one kernel of
+the sublayer or of its expert-parallel pieces computes and another uses is checked
+before the access, a failed check sets status bit 0x40 and skips the access. (The
+kernels of the top-k routing, combine and int8 calls have no such checks; what a caller
+gives them is checked in every build.) Load it with
 ``MOE_B200_LIBRARY=libmoe_b200_debug.so``.
 
 ``build_torch_calls`` compiles ``_torch_calls.so`` (csrc/torch_calls.cpp), the binding of

@@ -1,7 +1,8 @@
 // bounds.cuh — index checks of the MOE_DEBUG_BOUNDS build.
 //
-// The library's kernels index arrays with values that other kernels computed
-// (expert ids, permuted positions, per-expert row ranges). Built with
+// The kernels of the sublayer and of its expert-parallel pieces index arrays with
+// values that other kernels computed (expert ids, permuted positions, per-expert
+// row ranges). Built with
 // -DMOE_DEBUG_BOUNDS they check each such index before the access; a failed
 // check records kStatusBounds in the status word (read back through
 // moe_device_status) and the access is skipped, so a wrong index shows up as a

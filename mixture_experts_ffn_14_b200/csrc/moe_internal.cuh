@@ -30,7 +30,7 @@ enum : uint32_t {
   // range (|v| > 65504 rounds to infinity) in the conversion to fp16.
   kStatusFp16Range = 1u << 5,
   // MOE_DEBUG_BOUNDS builds: an index outside its array was caught and the
-  // access skipped.
+  // access skipped. moe_int8_product: counts that leave [0, R] were cut off.
   kStatusBounds = 1u << 6,
 };
 

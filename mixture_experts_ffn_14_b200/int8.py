@@ -37,7 +37,8 @@ def moe_int8_product(x, w, s, *, x_scale=None, index=None, counts=None, w_up=Non
     order; without it n must be 1. Rows of ``out`` [R, N] behind the last expert's are left
     as they were (an output that is not given starts as zeros then). ``out_dtype``: bf16
     (the default) or fp32. ``workspace``: uint8 tensor of moe_int8_workspace_size bytes;
-    moe_device_status reads its status word."""
+    moe_device_status reads its status word (bit 0x40: counts that are negative or run past
+    the rows were cut off)."""
     call = (_r._calls or _r._load()).int8_product
     args = (x, w, s, x_scale, index, counts, w_up, s_up, activation, gate, out, out_dtype, workspace)
     return call(*args) if stream is None else _r._on(stream, x, call, args)
