@@ -371,6 +371,27 @@ def test_route_backward_against_differences(kind, renorm):
     assert (np.abs(got.double().cpu().numpy() - num) <= lim).all()
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,E,k", [(40, 33, 4), (40, 256, 8), (6000, 16, 3)])
+def test_route_backward_reads_nothing_of_masked_and_padded_places(T, E, k, kind, renorm):
+    l = logits_of(T, E, torch.float32, T + E, masked=0.4)
+    n = T - T // 3
+    nt = torch.tensor([n], dtype=torch.int32, device=DEV)
+    idx = moe.moe_topk_route(l, k, score=SCORE[kind], dispatch=False, n_tokens=nt)["idx"]
+    g = gen(T)
+    gw, gs = torch.randn((T, k), generator=g, device=DEV), torch.randn((T, E), generator=g, device=DEV)
+    want = moe.moe_topk_route_backward(l, idx, gw, score=SCORE[kind], renormalize=renorm, grad_scores=gs, n_tokens=nt)
+    masked = ~(l > -float("inf"))
+    assert bool((idx[:n] < 0).any()) and bool(masked[:n].any()) and not bool(torch.isnan(want).any())
+    for odd in (float("nan"), float("inf")):
+        gw[idx < 0], gs[masked] = odd, odd
+        gs[n:] = odd
+        gw[n:] = odd
+        got = moe.moe_topk_route_backward(l, idx, gw, score=SCORE[kind], renormalize=renorm, grad_scores=gs, n_tokens=nt)
+        assert torch.equal(got, want) and bool((got[masked] == 0).all()) and bool((got[n:] == 0).all())
+
+
 def test_route_backward_odd_indices():
     # the same expert twice, and entries that are no expert
     l = logits_of(4, 16, torch.float32, 9)
